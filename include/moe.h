@@ -162,6 +162,14 @@ int32_t moe_route_z(const moe_config* cfg, const void* x, const float* w_r, cons
                     double* f, double* P, double* aux, double* z_loss,
                     void* ws, size_t ws_bytes, void* stream);
 
+/* moe_route_z plus the router's fp32 logits h = W_r x + b_r: logits [T, N]
+ * (required), the input of moe_balance_loss.  The other arguments and outputs
+ * are those of moe_route_z, bit for bit. */
+int32_t moe_route_logits(const moe_config* cfg, const void* x, const float* w_r, const float* b_r,
+                         int32_t* idx, float* gate, float* probs, float* logits,
+                         double* f, double* P, double* aux, double* z_loss,
+                         void* ws, size_t ws_bytes, void* stream);
+
 /* Gradient of L with respect to the gates, from the upstream dL/dout and the
  * un-gated expert outputs (out_t = sum_r gate_{t,r} E_{idx[t,r]}(x_t)):
  * dgate[t, r] = <dout_t, ye[offsets[idx[t,r]] + pos[t,r]]> for a kept
@@ -190,6 +198,71 @@ int32_t moe_router_backward(const moe_config* cfg, const void* x, const float* w
                             const int32_t* idx, const float* gate, const double* f, const float* dgate,
                             float* dh, float* dw_r, float* db_r, float* dx,
                             void* ws, size_t ws_bytes, void* stream);
+
+/* The products of moe_router_backward for any dL/dh: dh [T, N] fp32 is an input
+ * (for instance moe_router_backward's gate path with alpha = 0 plus
+ * moe_balance_loss_backward, accumulated), dw_r [N, d], db_r [N], dx [T, d] as
+ * there (each nullable). */
+int32_t moe_router_backward_dh(const moe_config* cfg, const void* x, const float* w_r, const float* dh,
+                               float* dw_r, float* db_r, float* dx, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- Load balancing over the sequences of a padded batch --------------------
+ * moe_route's loss takes f from the first choices of all T tokens.  These two
+ * calls generalise it: f counts all k choices, padded tokens are left out, and
+ * each sequence of the batch has its own loss.  Rows [seq_offsets[s],
+ * seq_offsets[s + 1]) of the batch are sequence s (non-decreasing, within
+ * [0, T]); rows before the first or behind the last sequence belong to none.
+ * mask [T] uint8: 0 leaves a token out (padding).  With p_t = softmax(h_t),
+ * n_s the tokens of s that count, n their sum, S' the sequences with n_s > 0:
+ *   counts[s][e] = how many of s's choices idx are e,  f = counts / (k n_s),
+ *   P[s][e] = (1 / n_s) sum_t p_te,
+ *   loss[0] = alpha N / S' sum_s sum_e f[s][e] P[s][e],
+ *   loss[1] = z_coef / n sum_t (log sum_e exp h_te)^2   (the router z-loss).
+ * One sequence, no mask and k = 1 give moe_route's aux.  Limits: 0 <= T < 2^28,
+ * 1 <= n_experts <= 512, 1 <= top_k <= min(16, n_experts), 1 <= n_seqs <= 2^20.
+ * A sum without terms is 0.  A logit of -inf is an expert that cannot be
+ * chosen (p = 0); a row without a finite logit counts in n_s and counts and
+ * adds 0 to P and both losses; NaN or +inf make their token's terms NaN.  Choices
+ * outside [0, N) are not counted.  Offsets outside [0, T] are clamped. */
+typedef struct {
+    int32_t T;            /* rows of the batch */
+    int32_t n_experts;    /* N */
+    int32_t top_k;        /* choices per token */
+    int32_t n_seqs;       /* S */
+    int32_t dtype;        /* moe_dtype of logits and dlogits */
+    float alpha;          /* balance loss weight */
+    float z_coef;         /* z-loss weight */
+    int32_t reserved;     /* 0 */
+    int64_t logits_ld;    /* row stride of logits in elements; 0 = n_experts */
+    int64_t dlogits_ld;   /* row stride of dlogits; 0 = n_experts */
+} moe_balance_config;
+
+/* Workspace bytes of moe_balance_loss (0 if invalid); moe_workspace_init it once.
+ * Calls that may run at the same time, captured graphs included, need a
+ * workspace each. */
+size_t moe_balance_workspace_bytes(const moe_balance_config* cfg);
+
+/* In:  logits [T, N] (dtype), idx [T, k] int32, mask [T] uint8 (nullable: every
+ *      token counts), seq_offsets [S + 1] int32 (nullable for S = 1: all rows).
+ * Out: loss [2] fp32, counts [S, N] int32, P [S, N] fp32 (nullable), tokens
+ *      [S + 2] int32: n_s of every sequence, n, S'.  Sums of p run in fp32 per
+ *      thread (at most 4096 tokens) and in fp64 beyond, in a fixed order. */
+int32_t moe_balance_loss(const moe_balance_config* cfg, const void* logits, const int32_t* idx,
+                         const uint8_t* mask, const int32_t* seq_offsets, float* loss, int32_t* counts,
+                         float* P, int32_t* tokens, void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of g0 loss[0] + g1 loss[1] with respect to the logits, the counts
+ * held constant:
+ *   dL/dh_tj = p_tj (a_j - sum_i p_ti a_i + g1 2 z_coef lse_t / n),
+ *   a_j = g0 alpha N f[s][j] / (S' n_s).
+ * In:  logits, mask, seq_offsets as in the forward; counts, tokens its outputs;
+ *      dloss [2] fp32 = (g0, g1) (nullable: 1, 1).
+ * Out: dlogits [T, N] (dtype): the gradient, 0 for a masked token; with
+ *      accumulate = 1 it is added to what is there (one rounding).  Rows that
+ *      belong to no sequence are left as they were. */
+int32_t moe_balance_loss_backward(const moe_balance_config* cfg, const void* logits, const uint8_t* mask,
+                                  const int32_t* seq_offsets, const int32_t* counts, const int32_t* tokens,
+                                  const float* dloss, void* dlogits, int32_t accumulate, void* stream);
 
 /* Backward of the expert FFN (bf16, on the tensor cores): gradients of
  * L = sum_t <dout_t, out_t> through the combine, the expert FFNs and their

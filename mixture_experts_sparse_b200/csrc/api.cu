@@ -245,7 +245,7 @@ const char* moe_status_string(int32_t status) {
 // to a later aux_reduce_block over their partials.
 static int32_t route_impl(const moe_config* cfg, const void* x, const float* w_r, const float* b_r, int32_t* idx,
                           float* gate, float* probs, double* f, double* P, double* aux, void* ws, size_t ws_bytes,
-                          void* stream, bool defer, double* z = nullptr) {
+                          void* stream, bool defer, double* z = nullptr, float* logits = nullptr) {
     int32_t st = validate(cfg);
     if (st != MOE_OK) return st;
     if (!req(w_r) || !opt(b_r) || !opt(probs) || !opt(f) || !opt(P) || !opt(aux)) return MOE_ERR_INVALID_ARG;
@@ -264,6 +264,7 @@ static int32_t route_impl(const moe_config* cfg, const void* x, const float* w_r
     a.idx = idx;
     a.gate = gate;
     a.probs = probs;
+    a.logits = logits;
     a.part_cnt = at<int32_t>(ws, L.part_cnt);
     a.part_psum = at<float>(ws, L.part_psum);
     a.part_z = at<double>(ws, L.part_z);
@@ -290,6 +291,16 @@ int32_t moe_route_z(const moe_config* cfg, const void* x, const float* w_r, cons
                     size_t ws_bytes, void* stream) {
     if (!opt(z_loss)) return MOE_ERR_INVALID_ARG;
     return route_impl(cfg, x, w_r, b_r, idx, gate, probs, f, P, aux, ws, ws_bytes, stream, false, z_loss);
+}
+
+int32_t moe_route_logits(const moe_config* cfg, const void* x, const float* w_r, const float* b_r, int32_t* idx,
+                         float* gate, float* probs, float* logits, double* f, double* P, double* aux, double* z_loss,
+                         void* ws, size_t ws_bytes, void* stream) {
+    if (!opt(z_loss)) return MOE_ERR_INVALID_ARG;
+    int32_t st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if (cfg->T > 0 ? !req(logits) : !opt(logits)) return MOE_ERR_INVALID_ARG;
+    return route_impl(cfg, x, w_r, b_r, idx, gate, probs, f, P, aux, ws, ws_bytes, stream, false, z_loss, logits);
 }
 
 static int32_t dispatch_impl(const moe_config* cfg, const void* x, const int32_t* idx, const float* gate,
@@ -421,15 +432,11 @@ int32_t moe_gate_grad(const moe_config* cfg, const void* dout, const void* ye, c
     return cuda_status(launch_gate_grad(a, (cudaStream_t)stream));
 }
 
-int32_t moe_router_backward(const moe_config* cfg, const void* x, const float* w_r, const float* probs,
-                            const int32_t* idx, const float* gate, const double* f, const float* dgate, float* dh,
-                            float* dw_r, float* db_r, float* dx, void* ws, size_t ws_bytes, void* stream) {
-    int32_t st = validate(cfg);
-    if (st != MOE_OK) return st;
-    if (!req(w_r) || !req(f) || !opt(dw_r) || !opt(db_r) || !opt(dx)) return MOE_ERR_INVALID_ARG;
-    if (cfg->T > 0 && (!req(x) || !req(probs) || !req(idx) || !req(gate) || !req(dgate) || !req(dh)))
-        return MOE_ERR_INVALID_ARG;
-    if ((st = check_ws(cfg, ws, ws_bytes)) != MOE_OK) return st;
+// The router's gradients: with probs == nullptr from a given dL/dh, otherwise dh
+// is formed first.
+static int32_t router_backward_impl(const moe_config* cfg, const void* x, const float* w_r, const float* probs,
+                                    const int32_t* idx, const float* gate, const double* f, const float* dgate,
+                                    float* dh, float* dw_r, float* db_r, float* dx, void* ws, void* stream) {
     const Layout L = layout_of(*cfg);
     RouterBwdArgs a{};
     a.x = x;
@@ -446,6 +453,7 @@ int32_t moe_router_backward(const moe_config* cfg, const void* x, const float* w
     a.N = cfg->n_experts;
     a.k = cfg->top_k;
     a.dh = dh;
+    a.dh_given = probs == nullptr;
     a.dw = dw_r;
     a.db = db_r;
     a.dx = dx;
@@ -460,6 +468,133 @@ int32_t moe_router_backward(const moe_config* cfg, const void* x, const float* w
     }
     a.status = &at<WsHeader>(ws, L.hdr)->status;
     return cuda_status(launch_router_backward(a, (cudaStream_t)stream));
+}
+
+int32_t moe_router_backward(const moe_config* cfg, const void* x, const float* w_r, const float* probs,
+                            const int32_t* idx, const float* gate, const double* f, const float* dgate, float* dh,
+                            float* dw_r, float* db_r, float* dx, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if (!req(w_r) || !req(f) || !opt(dw_r) || !opt(db_r) || !opt(dx)) return MOE_ERR_INVALID_ARG;
+    if (cfg->T > 0 && (!req(x) || !req(probs) || !req(idx) || !req(gate) || !req(dgate) || !req(dh)))
+        return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(cfg, ws, ws_bytes)) != MOE_OK) return st;
+    return router_backward_impl(cfg, x, w_r, probs, idx, gate, f, dgate, dh, dw_r, db_r, dx, ws, stream);
+}
+
+int32_t moe_router_backward_dh(const moe_config* cfg, const void* x, const float* w_r, const float* dh, float* dw_r,
+                               float* db_r, float* dx, void* ws, size_t ws_bytes, void* stream) {
+    int32_t st = validate(cfg);
+    if (st != MOE_OK) return st;
+    if (!req(w_r) || !opt(dw_r) || !opt(db_r) || !opt(dx)) return MOE_ERR_INVALID_ARG;
+    if (cfg->T > 0 && (!req(x) || !req(dh))) return MOE_ERR_INVALID_ARG;
+    if ((st = check_ws(cfg, ws, ws_bytes)) != MOE_OK) return st;
+    return router_backward_impl(cfg, x, w_r, nullptr, nullptr, nullptr, nullptr, nullptr, const_cast<float*>(dh), dw_r,
+                                db_r, dx, ws, stream);
+}
+
+// ---- balance loss over the sequences of a batch -----------------------------
+
+static int32_t balance_validate(const moe_balance_config* c) {
+    if (!c || c->T < 0 || c->n_experts < 1 || c->top_k < 1 || c->n_seqs < 1 || c->top_k > c->n_experts)
+        return MOE_ERR_INVALID_ARG;
+    if (c->dtype != MOE_F32 && c->dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(c->alpha) || !std::isfinite(c->z_coef)) return MOE_ERR_INVALID_ARG;
+    if ((c->logits_ld != 0 && c->logits_ld < c->n_experts) || (c->dlogits_ld != 0 && c->dlogits_ld < c->n_experts))
+        return MOE_ERR_INVALID_ARG;
+    if (c->T >= (1 << 28) || c->n_experts > 512 || c->top_k > 16 || c->n_seqs > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+struct BalanceLayout {
+    size_t hdr, slot_p, slot_c, slot_z, slot_n, seq_term, seq_z, total;
+};
+
+static BalanceLayout balance_layout(const moe_balance_config& c) {
+    BalanceLayout L{};
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        size_t o = off;
+        off += round_up(bytes, 256);
+        return o;
+    };
+    const size_t slots = (size_t)balance_slots(c.T, c.n_seqs), N = (size_t)c.n_experts, S = (size_t)c.n_seqs;
+    L.hdr = take(sizeof(WsHeader));
+    L.slot_p = take(4 * slots * N);
+    L.slot_c = take(4 * slots * N);
+    L.slot_z = take(8 * slots);
+    L.slot_n = take(4 * slots);
+    L.seq_term = take(8 * S);
+    L.seq_z = take(8 * S);
+    L.total = off;
+    return L;
+}
+
+static BalanceArgs balance_args(const moe_balance_config& c, const void* logits, const uint8_t* mask,
+                                const int32_t* seqs) {
+    BalanceArgs a{};
+    a.h = logits;
+    a.dtype = c.dtype;
+    a.ld = c.logits_ld ? c.logits_ld : c.n_experts;
+    a.dld = c.dlogits_ld ? c.dlogits_ld : c.n_experts;
+    a.mask = mask;
+    a.seqs = seqs;
+    a.T = c.T;
+    a.N = c.n_experts;
+    a.k = c.top_k;
+    a.S = c.n_seqs;
+    a.alpha = c.alpha;
+    a.z_coef = c.z_coef;
+    return a;
+}
+
+size_t moe_balance_workspace_bytes(const moe_balance_config* cfg) {
+    if (balance_validate(cfg) != MOE_OK) return 0;
+    return balance_layout(*cfg).total;
+}
+
+int32_t moe_balance_loss(const moe_balance_config* cfg, const void* logits, const int32_t* idx, const uint8_t* mask,
+                         const int32_t* seq_offsets, float* loss, int32_t* counts, float* P, int32_t* tokens, void* ws,
+                         size_t ws_bytes, void* stream) {
+    int32_t st = balance_validate(cfg);
+    if (st != MOE_OK) return st;
+    if (!req(loss) || !req(counts) || !req(tokens) || !opt(P) || !opt(mask)) return MOE_ERR_INVALID_ARG;
+    if (cfg->n_seqs > 1 ? !req(seq_offsets) : !opt(seq_offsets)) return MOE_ERR_INVALID_ARG;
+    if (cfg->T > 0 && (!req(logits) || !req(idx))) return MOE_ERR_INVALID_ARG;
+    const BalanceLayout L = balance_layout(*cfg);
+    if (!ws || !aligned(ws) || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    BalanceArgs a = balance_args(*cfg, logits, mask, seq_offsets);
+    a.idx = idx;
+    a.loss = loss;
+    a.counts = counts;
+    a.P = P;
+    a.tokens = tokens;
+    a.slot_p = at<float>(ws, L.slot_p);
+    a.slot_c = at<int32_t>(ws, L.slot_c);
+    a.slot_z = at<double>(ws, L.slot_z);
+    a.slot_n = at<int32_t>(ws, L.slot_n);
+    a.seq_term = at<double>(ws, L.seq_term);
+    a.seq_z = at<double>(ws, L.seq_z);
+    a.ticket = &at<WsHeader>(ws, L.hdr)->balance_ticket;
+    return cuda_status(launch_balance_loss(a, (cudaStream_t)stream));
+}
+
+int32_t moe_balance_loss_backward(const moe_balance_config* cfg, const void* logits, const uint8_t* mask,
+                                  const int32_t* seq_offsets, const int32_t* counts, const int32_t* tokens,
+                                  const float* dloss, void* dlogits, int32_t accumulate, void* stream) {
+    int32_t st = balance_validate(cfg);
+    if (st != MOE_OK) return st;
+    if (!req(counts) || !req(tokens) || !opt(dloss) || !opt(mask)) return MOE_ERR_INVALID_ARG;
+    if (cfg->n_seqs > 1 ? !req(seq_offsets) : !opt(seq_offsets)) return MOE_ERR_INVALID_ARG;
+    if (cfg->T > 0 && (!req(logits) || !req(dlogits))) return MOE_ERR_INVALID_ARG;
+    if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+    BalanceArgs a = balance_args(*cfg, logits, mask, seq_offsets);
+    a.counts = const_cast<int32_t*>(counts);
+    a.tokens = const_cast<int32_t*>(tokens);
+    a.dloss = dloss;
+    a.dh = dlogits;
+    a.accumulate = accumulate != 0;
+    return cuda_status(launch_balance_grad(a, (cudaStream_t)stream));
 }
 
 int32_t moe_dispatch(const moe_config* cfg, const void* x, const int32_t* idx, const float* gate, int32_t* pos,

@@ -23,7 +23,8 @@ struct WsHeader {
     int32_t scan_ticket;   // dynamic block index of the dispatch scan
     int32_t scan_done;     // finished-block counter of the dispatch scan
     int32_t route_ticket;  // finished-CTA counter of the tensor-core router
-    int32_t pad[60];
+    int32_t balance_ticket;  // finished-CTA counter of the balance loss
+    int32_t pad[59];
 };
 static_assert(sizeof(WsHeader) == 256, "header size");
 
@@ -224,6 +225,7 @@ struct RouterArgs {
     const void* x; int dtype; const float* w_r; const float* b_r;
     int64_t T; int d; int N; int k;
     int32_t* idx; float* gate; float* probs;
+    float* logits;                         // [T, N] (nullable)
     int32_t* part_cnt; float* part_psum;   // [nblk, N]
     double* f; double* P; double* aux; float alpha;
     double* part_z; double* z;             // router z-loss (z nullable; part_z [nblk] when z is set)
@@ -239,12 +241,31 @@ struct RouterBwdArgs {
     const float* probs; const int32_t* idx; const float* gate; const double* f; const float* dgate;
     float alpha; int64_t T; int d; int N; int k;
     float* dh;                        // [T, N]
+    bool dh_given;                    // dh is an input: only the products run
     float* dw; float* db; float* dx;  // [N, d], [N], [T, d] (each nullable)
     float* part_dw; float* part_db;   // [router_bwd_chunks(T), N, d], [.., N]
     // tensor-core path (bf16 x): workspace regions, see router_bwd_tc_bytes
     void* tc_adx; void* tc_adw; void* tc_bdx; int32_t* tc_offs; float* tc_part;
     int32_t* status;
 };
+
+// Balance loss over the sequences of a batch, and its gradient (balance.cu)
+struct BalanceArgs {
+    const void* h; int dtype; int64_t ld;     // logits [T, N], rows ld elements apart
+    const int32_t* idx;                       // [T, k]
+    const uint8_t* mask; const int32_t* seqs; // [T], [S + 1] (nullable)
+    int64_t T; int N; int k; int S; int tile;
+    float alpha; float z_coef;
+    float* loss; int32_t* counts; float* P; int32_t* tokens;
+    float* slot_p; int32_t* slot_c; double* slot_z; int32_t* slot_n;   // [balance_slots(T, S)](, N)
+    double* seq_term; double* seq_z;          // [S]
+    int32_t* ticket;
+    const float* dloss; void* dh; int64_t dld; bool accumulate;
+};
+int64_t balance_slots(int64_t T, int S);
+cudaError_t launch_balance_loss(BalanceArgs a, cudaStream_t s);
+cudaError_t launch_balance_grad(BalanceArgs a, cudaStream_t s);
+
 int router_bwd_chunks(int64_t T);
 // tensor-core router backward: padded experts (a multiple of 16), tokens per
 // dW_r chunk (at most 128 chunks), and the chunk count

@@ -47,6 +47,7 @@ __global__ void __launch_bounds__(kThreads)
 router_kernel(const XT* __restrict__ x, const float* __restrict__ w_r, const float* __restrict__ b_r,
               int64_t T, int d, int N, int k,
               int32_t* __restrict__ idx, float* __restrict__ gate, float* __restrict__ probs,
+              float* __restrict__ logits,
               int32_t* __restrict__ part_cnt, float* __restrict__ part_psum, double* __restrict__ part_z) {
     using S = RouterShape<TE, EG, kTT>;
     constexpr int VEC = 16 / sizeof(XT);          // elements per 16-byte load
@@ -163,6 +164,10 @@ router_kernel(const XT* __restrict__ x, const float* __restrict__ w_r, const flo
     constexpr int MPL = (S::NP + 31) / 32;
     const int64_t rem_t = T - t0;
     const int tb_valid = rem_t < (int64_t)S::TB ? (int)rem_t : S::TB;
+    if (logits) {   // before the rows are overwritten with probabilities
+        for (int q = tid; q < tb_valid * N; q += kThreads) logits[t0 * N + q] = lg[q / N * (S::NP + 1) + q % N];
+        __syncthreads();
+    }
     double zacc = 0.0;   // sum over this warp's (thread's) tokens of log-sum-exp^2
     if (S::NP <= 32) {
         // few experts: one thread per token, its logits in registers (no
@@ -404,7 +409,7 @@ cudaError_t launch_router_t(const RouterArgs& a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     if (nblk > 0) {
         err = launch_k(kern, dim3((unsigned)nblk), dim3(kThreads), smem, s, 1, reinterpret_cast<const XT*>(a.x), a.w_r,
-                       a.b_r, a.T, a.d, a.N, a.k, a.idx, a.gate, a.probs, a.part_cnt, a.part_psum,
+                       a.b_r, a.T, a.d, a.N, a.k, a.idx, a.gate, a.probs, a.logits, a.part_cnt, a.part_psum,
                        a.z ? a.part_z : nullptr);
         if (err != cudaSuccess) return err;
     }

@@ -378,9 +378,10 @@ cudaError_t launch_router_backward(const RouterBwdArgs& a, cudaStream_t s) {
         if (e == cudaSuccess && a.db) e = cudaMemsetAsync(a.db, 0, sizeof(float) * a.N, s);
         return e;
     }
-    cudaError_t err = launch_k(router_bwd_dh_kernel, dim3((unsigned)((a.T + 8 * kDhTokens - 1) / (8 * kDhTokens))),
-                               dim3(256), 0, s, 1, a.probs,
-                               a.idx, a.gate, a.dgate, a.f, a.alpha, a.T, a.N, a.k, a.dh);
+    cudaError_t err = cudaSuccess;
+    if (!a.dh_given)
+        err = launch_k(router_bwd_dh_kernel, dim3((unsigned)((a.T + 8 * kDhTokens - 1) / (8 * kDhTokens))), dim3(256),
+                       0, s, 1, a.probs, a.idx, a.gate, a.dgate, a.f, a.alpha, a.T, a.N, a.k, a.dh);
     if (err != cudaSuccess) return err;
     if (a.dtype == MOE_BF16 && a.tc_adx && (a.dw || a.db || a.dx)) {
         // the contractions on the tensor cores

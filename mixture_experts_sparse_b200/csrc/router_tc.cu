@@ -122,6 +122,7 @@ struct RtParams {
     int32_t* idx;
     float* gate;
     float* probs;
+    float* logits;
     int32_t* part_cnt;    // [N, Gp] per-CTA top-1 counts (Gp = gridDim.x rounded up to 4)
     float* part_psum;     // [N, Gp] per-CTA sums of p
     double* f;            // outputs of the aux loss (nullable)
@@ -395,6 +396,11 @@ router_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant_
             tc_fence_before();
             mbar_arrive_cluster_relaxed(acc ? tempty_leader1 : tempty_leader0);   // the accumulator is free again
 
+            if (p.logits && valid) {
+#pragma unroll
+                for (int e = 0; e < NP; ++e)
+                    if (e < N) p.logits[t * N + e] = v[e];
+            }
             // first choice: the largest logit, lowest index among equals
             const float m = tree_max(v);
             const int i1 = tree_first(v, m);
@@ -540,6 +546,7 @@ cudaError_t run_router_tc(const RouterArgs& a, cudaStream_t s, int sms) {
     p.idx = a.idx;
     p.gate = a.gate;
     p.probs = a.probs;
+    p.logits = a.logits;
     p.part_cnt = a.part_cnt;
     p.part_psum = a.part_psum;
     p.f = a.f;

@@ -26,6 +26,13 @@ class MoeConfig(ctypes.Structure):
                 ("priority", ctypes.c_int32)]
 
 
+class MoeBalanceConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("n_seqs", ctypes.c_int32), ("dtype", ctypes.c_int32), ("alpha", ctypes.c_float),
+                ("z_coef", ctypes.c_float), ("reserved", ctypes.c_int32), ("logits_ld", ctypes.c_int64),
+                ("dlogits_ld", ctypes.c_int64)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, status):
         self.status = status
@@ -41,6 +48,12 @@ _SIGS = {
     "moe_workspace_init": ([_P, ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_route": ([ctypes.POINTER(MoeConfig)] + [_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_route_z": ([ctypes.POINTER(MoeConfig)] + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_route_logits": ([ctypes.POINTER(MoeConfig)] + [_P] * 12 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_router_backward_dh": ([ctypes.POINTER(MoeConfig)] + [_P] * 7 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_balance_workspace_bytes": ([ctypes.POINTER(MoeBalanceConfig)], ctypes.c_size_t),
+    "moe_balance_loss": ([ctypes.POINTER(MoeBalanceConfig)] + [_P] * 9 + [ctypes.c_size_t, _P], ctypes.c_int32),
+    "moe_balance_loss_backward": ([ctypes.POINTER(MoeBalanceConfig)] + [_P] * 7 + [ctypes.c_int32, _P],
+                                  ctypes.c_int32),
     "moe_dispatch_ntlb": ([ctypes.POINTER(MoeConfig)] + [_P] * 13 + [ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_router_backward": ([ctypes.POINTER(MoeConfig)] + [_P] * 12 + [ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_gate_grad": ([ctypes.POINTER(MoeConfig)] + [_P] * 8, ctypes.c_int32),
@@ -96,6 +109,13 @@ def config(T, d_model, d_ff, n_experts, top_k, capacity, dtype="bf16", act="relu
                      MOE_SWIGLU if act in ("swiglu", MOE_SWIGLU) else MOE_RELU, float(alpha), order)
 
 
+def balance_config(T, n_experts, top_k, n_seqs=1, dtype="f32", alpha=1e-2, z_coef=0.0, logits_ld=0, dlogits_ld=0):
+    """moe_balance_config.  logits_ld / dlogits_ld: row strides in elements (0: rows are dense)."""
+    return MoeBalanceConfig(int(T), int(n_experts), int(top_k), int(n_seqs),
+                            MOE_BF16 if dtype in ("bf16", MOE_BF16) else MOE_F32, float(alpha), float(z_coef), 0,
+                            int(logits_ld), int(dlogits_ld))
+
+
 def _p(t):
     if t is None:
         return None
@@ -146,6 +166,21 @@ def new_workspace(cfg, device="cuda", stream=None):
     return ws
 
 
+def moe_balance_workspace_bytes(cfg):
+    return int(lib().moe_balance_workspace_bytes(ctypes.byref(cfg)))
+
+
+def new_balance_workspace(cfg, device="cuda", stream=None):
+    """Allocate (torch) and initialise a workspace of moe_balance_loss."""
+    import torch
+    nbytes = moe_balance_workspace_bytes(cfg)
+    if nbytes == 0:
+        raise ValueError("invalid balance-loss configuration")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    check(moe_workspace_init(ws, stream))
+    return ws
+
+
 def moe_status_string(status):
     return lib().moe_status_string(int(status)).decode()
 
@@ -158,6 +193,27 @@ def moe_route(cfg, x, w_r, b_r, idx, gate, probs, f, P, aux, ws, stream=None):
 def moe_route_z(cfg, x, w_r, b_r, idx, gate, probs, f, P, aux, z_loss, ws, stream=None):
     return lib().moe_route_z(ctypes.byref(cfg), _p(x), _p(w_r), _p(b_r), _p(idx), _p(gate), _p(probs),
                              _p(f), _p(P), _p(aux), _p(z_loss), _p(ws), _nbytes(ws), _s(stream))
+
+
+def moe_route_logits(cfg, x, w_r, b_r, idx, gate, probs, logits, f, P, aux, z_loss, ws, stream=None):
+    return lib().moe_route_logits(ctypes.byref(cfg), _p(x), _p(w_r), _p(b_r), _p(idx), _p(gate), _p(probs),
+                                  _p(logits), _p(f), _p(P), _p(aux), _p(z_loss), _p(ws), _nbytes(ws), _s(stream))
+
+
+def moe_balance_loss(cfg, logits, idx, mask, seq_offsets, loss, counts, P, tokens, ws, stream=None):
+    return lib().moe_balance_loss(ctypes.byref(cfg), _p(logits), _p(idx), _p(mask), _p(seq_offsets), _p(loss),
+                                  _p(counts), _p(P), _p(tokens), _p(ws), _nbytes(ws), _s(stream))
+
+
+def moe_balance_loss_backward(cfg, logits, mask, seq_offsets, counts, tokens, dloss, dlogits, accumulate=False,
+                              stream=None):
+    return lib().moe_balance_loss_backward(ctypes.byref(cfg), _p(logits), _p(mask), _p(seq_offsets), _p(counts),
+                                           _p(tokens), _p(dloss), _p(dlogits), int(accumulate), _s(stream))
+
+
+def moe_router_backward_dh(cfg, x, w_r, dh, dw_r, db_r, dx, ws, stream=None):
+    return lib().moe_router_backward_dh(ctypes.byref(cfg), _p(x), _p(w_r), _p(dh), _p(dw_r), _p(db_r), _p(dx),
+                                        _p(ws), _nbytes(ws), _s(stream))
 
 
 def moe_gate_grad(cfg, dout, ye, idx, pos, drop, offsets, dgate, stream=None):
