@@ -379,6 +379,45 @@ int32_t moe_expert_ffn(const moe_config* cfg, const void* xe, const int32_t* off
                        const void* w2, const void* b2, void* ye,
                        void* ws, size_t ws_bytes, void* stream);
 
+/* ---- 4-bit expert weights with group scales ---------------------------------
+ * A matrix [rows, k] (k a multiple of 16) is stored as packed rows of
+ * moe_w4_row_bytes(k) bytes and bf16 scales [ceil(k / group), rows]; group is
+ * 32, 64 or 128 consecutive weights of a row (the last group may be shorter).
+ * A weight stands for (c - 8) * scale, c its 4-bit code.  Packed row: blocks
+ * of 128 weights, 64 bytes each, the last one padded with code 8; 32-bit word
+ * 4 t + j of a block (t, j = 0..3) holds its weights n = 32 j + 8 t ... + 7:
+ * weight n + 2 i in bits 4 i ... 4 i + 3, weight n + 2 i + 1 in bits 16 + 4 i ...
+ * (i = 0..3).  mats matrices follow one another: q [mats, rows, row bytes],
+ * scale [mats, ceil(k / group), rows]. */
+size_t moe_w4_row_bytes(int64_t k);
+
+/* scale = bf16(max |w| / 7) over the group, code = 8 + rint(w / scale) (ties to
+ * even, both decided as in exact arithmetic; codes 1 to 15).  A group of zeros
+ * has scale 0; one that holds an infinity or NaN has scale NaN and stands for
+ * NaN as a whole.  In: w [mats, rows, k] (dtype: MOE_F32 or MOE_BF16).  Out: q,
+ * scale.  MOE_ERR_UNSUPPORTED for another group or k % 16 != 0. */
+int32_t moe_quantize_w4(int64_t mats, int64_t rows, int64_t k, int32_t group, int32_t dtype, const void* w,
+                        uint8_t* q, void* scale, void* stream);
+
+/* The weights that q and scale stand for: w [mats, rows, k] (dtype), the product
+ * rounded once (exact for MOE_F32). */
+int32_t moe_dequantize_w4(int64_t mats, int64_t rows, int64_t k, int32_t group, int32_t dtype, const uint8_t* q,
+                          const void* scale, void* w, void* stream);
+
+/* Workspace bytes of moe_expert_ffn_w4 and moe_forward_w4 (0 if the config is
+ * invalid or not MOE_BF16); it also serves every call of moe_workspace_bytes. */
+size_t moe_w4_workspace_bytes(const moe_config* cfg);
+
+/* moe_expert_ffn on 4-bit weights: w1, w3 [N, d_ff, d] and w2 [N, d, d_ff] as
+ * (q1, s1), (q3, s3; SwiGLU), (q2, s2), all with the same group; the biases are
+ * bf16 (nullable).  bf16 rows in and out (MOE_F32: MOE_ERR_UNSUPPORTED).  Weights
+ * enter as integers times their scale, unrounded, with fp32 accumulation; rows of
+ * ye past offsets[N] are left as they were. */
+int32_t moe_expert_ffn_w4(const moe_config* cfg, int32_t group, const void* xe, const int32_t* offsets,
+                          const uint8_t* q1, const void* s1, const void* b1, const uint8_t* q3, const void* s3,
+                          const void* b3, const uint8_t* q2, const void* s2, const void* b2, void* ye,
+                          void* ws, size_t ws_bytes, void* stream);
+
 /* Gate-scaled combine back to token order (row A7).
  * out[t] = sum over r with drop[t,r] == 0 of gate[t,r] * ye[offsets[idx[t,r]] +
  * pos[t,r]], accumulated in fp32 and rounded once; zero if every assignment of
@@ -414,6 +453,17 @@ int32_t moe_forward(const moe_config* cfg, const void* x, const float* w_r, cons
                     int32_t* counts, int32_t* kept, int32_t* offsets,
                     double* f, double* P, double* aux,
                     void* ws, size_t ws_bytes, void* stream);
+
+/* moe_forward on 4-bit expert weights (see moe_expert_ffn_w4): route, dispatch,
+ * experts, combine, from a single decoded token to a batch.  The arguments are
+ * moe_forward's with the weights of moe_expert_ffn_w4; the workspace is
+ * moe_w4_workspace_bytes(cfg) bytes. */
+int32_t moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, const float* w_r, const float* b_r,
+                       const uint8_t* q1, const void* s1, const void* b1, const uint8_t* q3, const void* s3,
+                       const void* b3, const uint8_t* q2, const void* s2, const void* b2, void* out,
+                       int32_t* idx, float* gate, int32_t* pos, uint8_t* drop, int32_t* counts, int32_t* kept,
+                       int32_t* offsets, double* f, double* P, double* aux,
+                       void* ws, size_t ws_bytes, void* stream);
 
 /* moe_forward, plus stage timing for profiling: `events` points to 6 cudaEvent_t
  * handles (passed as void*, created by the caller; any entry may be NULL) that

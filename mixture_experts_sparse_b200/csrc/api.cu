@@ -10,6 +10,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "w4.cuh"
 
 namespace moe {
 
@@ -703,6 +704,104 @@ int32_t moe_expert_ffn(const moe_config* cfg, const void* xe, const int32_t* off
                     (cudaStream_t)stream);
 }
 
+// ---- 4-bit expert weights ----------------------------------------------------
+
+static bool w4_group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
+
+// the layer workspace, then what H's rounding to bf16 left (h_lo)
+static size_t w4_lo_offset(const Layout& L) { return L.total; }
+static size_t w4_total(const moe_config& c, const Layout& L) {
+    const size_t R = (size_t)(L.rows > 0 ? L.rows : 1);
+    return L.total + round_up(2 * R * (size_t)c.d_ff, 256);
+}
+
+size_t moe_w4_row_bytes(int64_t k) { return k < 0 ? 0 : (size_t)w4_row_bytes(k); }
+
+size_t moe_w4_workspace_bytes(const moe_config* cfg) {
+    if (validate(cfg) != MOE_OK || cfg->dtype != MOE_BF16) return 0;
+    return w4_total(*cfg, layout_of(*cfg));
+}
+
+static int32_t w4_check(int64_t mats, int64_t rows, int64_t k, int32_t group, int32_t dtype, const void* w,
+                        const void* q, const void* scale) {
+    if (mats < 0 || rows < 0 || k < 1) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if (!w4_group_ok(group) || k % 16 != 0 || k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (mats >= (1LL << 31) || rows >= (1LL << 31) || (mats > 0 && rows > (1LL << 34) / mats)) return MOE_ERR_UNSUPPORTED;
+    if (mats > 0 && rows > 0 && (!req(w) || !req(q) || !req(scale))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+int32_t moe_quantize_w4(int64_t mats, int64_t rows, int64_t k, int32_t group, int32_t dtype, const void* w, uint8_t* q,
+                        void* scale, void* stream) {
+    const int32_t st = w4_check(mats, rows, k, group, dtype, w, q, scale);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_w4_quantize(mats, rows, k, group, dtype, w, q, static_cast<uint16_t*>(scale),
+                                          (cudaStream_t)stream));
+}
+
+int32_t moe_dequantize_w4(int64_t mats, int64_t rows, int64_t k, int32_t group, int32_t dtype, const uint8_t* q,
+                          const void* scale, void* w, void* stream) {
+    const int32_t st = w4_check(mats, rows, k, group, dtype, w, q, scale);
+    if (st != MOE_OK) return st;
+    return cuda_status(launch_w4_dequantize(mats, rows, k, group, dtype, q, static_cast<const uint16_t*>(scale), w,
+                                            (cudaStream_t)stream));
+}
+
+struct W4Weights {
+    int32_t group;
+    const uint8_t *q1, *q3, *q2;
+    const void *s1, *s3, *s2, *b1, *b3, *b2;
+};
+
+static int32_t w4_check_weights(const moe_config* cfg, const W4Weights& w) {
+    if (cfg->dtype != MOE_BF16 || !w4_group_ok(w.group)) return MOE_ERR_UNSUPPORTED;
+    if (!req(w.q1) || !req(w.s1) || !req(w.q2) || !req(w.s2) || !opt(w.b1) || !opt(w.b3) || !opt(w.b2))
+        return MOE_ERR_INVALID_ARG;
+    if (cfg->act == MOE_SWIGLU ? (!req(w.q3) || !req(w.s3)) : (!opt(w.q3) || !opt(w.s3))) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+static int32_t w4_ffn_impl(const moe_config* cfg, const W4Weights& w, const void* xe, const int32_t* offsets, void* ye,
+                           void* ws, cudaStream_t s) {
+    const Layout L = layout_of(*cfg);
+    if (L.rows <= 0) return MOE_OK;   // nothing can be kept
+    W4FfnArgs a{};
+    a.act = cfg->act;
+    a.N = cfg->n_experts;
+    a.d = cfg->d_model;
+    a.d_ff = cfg->d_ff;
+    a.group = w.group;
+    a.R_cap = L.rows;
+    a.xe = static_cast<const __nv_bfloat16*>(xe);
+    a.offsets = offsets;
+    a.w1 = W4Mat{w.q1, static_cast<const uint16_t*>(w.s1)};
+    a.w3 = W4Mat{w.q3, static_cast<const uint16_t*>(w.s3)};
+    a.w2 = W4Mat{w.q2, static_cast<const uint16_t*>(w.s2)};
+    a.b1 = static_cast<const __nv_bfloat16*>(w.b1);
+    a.b3 = static_cast<const __nv_bfloat16*>(w.b3);
+    a.b2 = static_cast<const __nv_bfloat16*>(w.b2);
+    a.h = at<__nv_bfloat16>(ws, L.h);
+    a.h_lo = at<__nv_bfloat16>(ws, w4_lo_offset(L));
+    a.ye = static_cast<__nv_bfloat16*>(ye);
+    a.hdr = at<WsHeader>(ws, L.hdr);
+    return cuda_status(launch_w4_ffn(a, s));
+}
+
+int32_t moe_expert_ffn_w4(const moe_config* cfg, int32_t group, const void* xe, const int32_t* offsets,
+                          const uint8_t* q1, const void* s1, const void* b1, const uint8_t* q3, const void* s3,
+                          const void* b3, const uint8_t* q2, const void* s2, const void* b2, void* ye, void* ws,
+                          size_t ws_bytes, void* stream) {
+    int32_t st = validate(cfg);
+    if (st != MOE_OK) return st;
+    const W4Weights w{group, q1, q3, q2, s1, s3, s2, b1, b3, b2};
+    if ((st = w4_check_weights(cfg, w)) != MOE_OK) return st;
+    if (!req(offsets)) return MOE_ERR_INVALID_ARG;
+    if (compact_rows(*cfg) > 0 && (!req(xe) || !req(ye))) return MOE_ERR_INVALID_ARG;
+    if (!ws || !aligned(ws) || ws_bytes < w4_total(*cfg, layout_of(*cfg))) return MOE_ERR_WORKSPACE;
+    return w4_ffn_impl(cfg, w, xe, offsets, ye, ws, (cudaStream_t)stream);
+}
+
 static int32_t combine_impl(const moe_config* cfg, const void* ye, const int32_t* idx, const int32_t* pos,
                             const uint8_t* drop, const float* gate, const int32_t* offsets,
                             const int32_t* claim_base, const int32_t* counts, void* out, void* stream) {
@@ -747,11 +846,18 @@ static int32_t forward_impl(const moe_config* cfg, const void* x, const float* w
                             const void* w1, const void* b1, const void* w3, const void* b3, const void* w2,
                             const void* b2, void* out, int32_t* idx, float* gate, int32_t* pos, uint8_t* drop,
                             int32_t* counts, int32_t* kept, int32_t* offsets, double* f, double* P, double* aux,
-                            void* ws, size_t ws_bytes, cudaStream_t s, void* const* events) {
+                            void* ws, size_t ws_bytes, cudaStream_t s, void* const* events,
+                            const W4Weights* w4 = nullptr) {
     int32_t st = validate(cfg);
     if (st != MOE_OK) return st;
-    if (!req(w_r) || !req(w1) || !req(w2) || !opt(b_r) || !opt(b1) || !opt(b2) || !opt(b3)) return MOE_ERR_INVALID_ARG;
-    if (cfg->act == MOE_SWIGLU ? !req(w3) : !opt(w3)) return MOE_ERR_INVALID_ARG;
+    if (!req(w_r) || !opt(b_r)) return MOE_ERR_INVALID_ARG;
+    if (w4) {   // 4-bit experts: w1, w3, w2 and the biases come in w4
+        if ((st = w4_check_weights(cfg, *w4)) != MOE_OK) return st;
+        if (!ws || !aligned(ws) || ws_bytes < w4_total(*cfg, layout_of(*cfg))) return MOE_ERR_WORKSPACE;
+    } else {
+        if (!req(w1) || !req(w2) || !opt(b1) || !opt(b2) || !opt(b3)) return MOE_ERR_INVALID_ARG;
+        if (cfg->act == MOE_SWIGLU ? !req(w3) : !opt(w3)) return MOE_ERR_INVALID_ARG;
+    }
     if (cfg->T > 0 && (!req(x) || !req(out))) return MOE_ERR_INVALID_ARG;
     if (!opt(idx) || !opt(gate) || !opt(pos) || !opt(drop) || !opt(counts) || !opt(kept) || !opt(offsets) || !opt(f) ||
         !opt(P) || !opt(aux))
@@ -796,7 +902,7 @@ static int32_t forward_impl(const moe_config* cfg, const void* x, const float* w
     if (!mark(1)) return MOE_ERR_CUDA;
     // top-1 bf16: the second GEMM scatters gate * E(x) into out; dispatch zeroes
     // the rows of dropped tokens.  Otherwise expert outputs go through the combine.
-    const bool fused = cfg->dtype == MOE_BF16 && cfg->top_k == 1;
+    const bool fused = cfg->dtype == MOE_BF16 && cfg->top_k == 1 && !w4;
     // re-routing overwrites idx and gate with the expert each token finally uses and its probability
     st = ntlb ? ntlb_impl(cfg, x, probs_ws, idx, gate, pos, drop, counts, kept, offsets, row_token, row_gate, xe,
                           fused ? out : nullptr, ws, s, aa.G > 0 ? &aa : nullptr)
@@ -804,8 +910,9 @@ static int32_t forward_impl(const moe_config* cfg, const void* x, const float* w
                               fused ? out : nullptr, ws, s, nullptr, aa.G > 0 ? &aa : nullptr);
     if (st != MOE_OK) return st;
     if (!mark(2)) return MOE_ERR_CUDA;
-    st = ffn_impl(cfg, xe, offsets, w1, b1, w3, b3, w2, b2, ye, fused ? out : nullptr, row_token, row_gate, ws, s,
-                  events ? events + 3 : nullptr);
+    st = w4 ? w4_ffn_impl(cfg, *w4, xe, offsets, ye, ws, s)
+            : ffn_impl(cfg, xe, offsets, w1, b1, w3, b3, w2, b2, ye, fused ? out : nullptr, row_token, row_gate, ws, s,
+                       events ? events + 3 : nullptr);
     if (st != MOE_OK) return st;
     if (!mark(4)) return MOE_ERR_CUDA;
     if (!fused) {
@@ -843,6 +950,16 @@ int32_t moe_forward_events(const moe_config* cfg, const void* x, const float* w_
                            void* ws, size_t ws_bytes, void* stream, void* const* events) {
     return forward_impl(cfg, x, w_r, b_r, w1, b1, w3, b3, w2, b2, out, idx, gate, pos, drop, counts, kept, offsets,
                         f, P, aux, ws, ws_bytes, (cudaStream_t)stream, events);
+}
+
+int32_t moe_forward_w4(const moe_config* cfg, int32_t group, const void* x, const float* w_r, const float* b_r,
+                       const uint8_t* q1, const void* s1, const void* b1, const uint8_t* q3, const void* s3,
+                       const void* b3, const uint8_t* q2, const void* s2, const void* b2, void* out, int32_t* idx,
+                       float* gate, int32_t* pos, uint8_t* drop, int32_t* counts, int32_t* kept, int32_t* offsets,
+                       double* f, double* P, double* aux, void* ws, size_t ws_bytes, void* stream) {
+    const W4Weights w{group, q1, q3, q2, s1, s3, s2, b1, b3, b2};
+    return forward_impl(cfg, x, w_r, b_r, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, out, idx, gate, pos,
+                        drop, counts, kept, offsets, f, P, aux, ws, ws_bytes, (cudaStream_t)stream, nullptr, &w);
 }
 
 // ---- expert FFN backward ---------------------------------------------------

@@ -54,6 +54,14 @@ _SIGS = {
     "moe_balance_loss": ([ctypes.POINTER(MoeBalanceConfig)] + [_P] * 9 + [ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_balance_loss_backward": ([ctypes.POINTER(MoeBalanceConfig)] + [_P] * 7 + [ctypes.c_int32, _P],
                                   ctypes.c_int32),
+    "moe_w4_row_bytes": ([ctypes.c_int64], ctypes.c_size_t),
+    "moe_quantize_w4": ([ctypes.c_int64] * 3 + [ctypes.c_int32] * 2 + [_P] * 4, ctypes.c_int32),
+    "moe_dequantize_w4": ([ctypes.c_int64] * 3 + [ctypes.c_int32] * 2 + [_P] * 4, ctypes.c_int32),
+    "moe_w4_workspace_bytes": ([ctypes.POINTER(MoeConfig)], ctypes.c_size_t),
+    "moe_expert_ffn_w4": ([ctypes.POINTER(MoeConfig), ctypes.c_int32] + [_P] * 13 + [ctypes.c_size_t, _P],
+                          ctypes.c_int32),
+    "moe_forward_w4": ([ctypes.POINTER(MoeConfig), ctypes.c_int32] + [_P] * 24 + [ctypes.c_size_t, _P],
+                       ctypes.c_int32),
     "moe_dispatch_ntlb": ([ctypes.POINTER(MoeConfig)] + [_P] * 13 + [ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_router_backward": ([ctypes.POINTER(MoeConfig)] + [_P] * 12 + [ctypes.c_size_t, _P], ctypes.c_int32),
     "moe_gate_grad": ([ctypes.POINTER(MoeConfig)] + [_P] * 8, ctypes.c_int32),
@@ -112,7 +120,7 @@ def config(T, d_model, d_ff, n_experts, top_k, capacity, dtype="bf16", act="relu
 def balance_config(T, n_experts, top_k, n_seqs=1, dtype="f32", alpha=1e-2, z_coef=0.0, logits_ld=0, dlogits_ld=0):
     """moe_balance_config.  logits_ld / dlogits_ld: row strides in elements (0: rows are dense)."""
     return MoeBalanceConfig(int(T), int(n_experts), int(top_k), int(n_seqs),
-                            MOE_BF16 if dtype in ("bf16", MOE_BF16) else MOE_F32, float(alpha), float(z_coef), 0,
+                            _dt(dtype), float(alpha), float(z_coef), 0,
                             int(logits_ld), int(dlogits_ld))
 
 
@@ -271,6 +279,54 @@ def moe_aux_shards(n_shards, n_experts, shard_tokens, f_all, P_all, alpha, f, P,
 def moe_expert_ffn(cfg, xe, offsets, w1, b1, w3, b3, w2, b2, ye, ws, stream=None):
     return lib().moe_expert_ffn(ctypes.byref(cfg), _p(xe), _p(offsets), _p(w1), _p(b1), _p(w3), _p(b3),
                                 _p(w2), _p(b2), _p(ye), _p(ws), _nbytes(ws), _s(stream))
+
+
+# ---- 4-bit expert weights
+
+def _dt(dtype):
+    return MOE_BF16 if dtype in ("bf16", MOE_BF16) else MOE_F32
+
+
+def moe_w4_row_bytes(k):
+    return int(lib().moe_w4_row_bytes(int(k)))
+
+
+def moe_quantize_w4(mats, rows, k, group, dtype, w, q, scale, stream=None):
+    return lib().moe_quantize_w4(int(mats), int(rows), int(k), int(group), _dt(dtype), _p(w), _p(q), _p(scale),
+                                 _s(stream))
+
+
+def moe_dequantize_w4(mats, rows, k, group, dtype, q, scale, w, stream=None):
+    return lib().moe_dequantize_w4(int(mats), int(rows), int(k), int(group), _dt(dtype), _p(q), _p(scale), _p(w),
+                                   _s(stream))
+
+
+def moe_w4_workspace_bytes(cfg):
+    return int(lib().moe_w4_workspace_bytes(ctypes.byref(cfg)))
+
+
+def new_w4_workspace(cfg, device="cuda", stream=None):
+    """Allocate (torch) and initialise a workspace of the 4-bit expert calls."""
+    import torch
+    nbytes = moe_w4_workspace_bytes(cfg)
+    if nbytes == 0:
+        raise ValueError("invalid layer configuration for 4-bit experts")
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    check(moe_workspace_init(ws, stream))
+    return ws
+
+
+def moe_expert_ffn_w4(cfg, group, xe, offsets, q1, s1, b1, q3, s3, b3, q2, s2, b2, ye, ws, stream=None):
+    return lib().moe_expert_ffn_w4(ctypes.byref(cfg), int(group), _p(xe), _p(offsets), _p(q1), _p(s1), _p(b1), _p(q3),
+                                   _p(s3), _p(b3), _p(q2), _p(s2), _p(b2), _p(ye), _p(ws), _nbytes(ws), _s(stream))
+
+
+def moe_forward_w4(cfg, group, x, w_r, b_r, q1, s1, b1, q3, s3, b3, q2, s2, b2, out, idx=None, gate=None, pos=None,
+                   drop=None, counts=None, kept=None, offsets=None, f=None, P=None, aux=None, ws=None, stream=None):
+    return lib().moe_forward_w4(ctypes.byref(cfg), int(group), _p(x), _p(w_r), _p(b_r), _p(q1), _p(s1), _p(b1),
+                                _p(q3), _p(s3), _p(b3), _p(q2), _p(s2), _p(b2), _p(out), _p(idx), _p(gate), _p(pos),
+                                _p(drop), _p(counts), _p(kept), _p(offsets), _p(f), _p(P), _p(aux), _p(ws),
+                                _nbytes(ws), _s(stream))
 
 
 def moe_combine(cfg, ye, idx, pos, drop, gate, offsets, out, stream=None):
