@@ -125,20 +125,28 @@ def balance_config(T, n_experts, top_k, n_seqs=1, dtype="f32", alpha=1e-2, z_coe
 
 
 def _p(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr())
+    # c_void_p arguments take plain integers; wrapping each would cost more than the kernel launch
+    if t is None or isinstance(t, int):
+        return t
+    return t.data_ptr()
+
+
+_current_stream = None
 
 
 def _s(stream):
+    """The raw stream: torch's current one by default, read without building a
+    torch Stream object (3.5 us a call, against 0.2)."""
+    global _current_stream
     if stream is None:
-        import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _current_stream is None:
+            import torch
+            raw, device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
+            _current_stream = lambda: raw(device())  # noqa: E731
+        return _current_stream()
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _nbytes(ws):
