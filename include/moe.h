@@ -129,8 +129,8 @@ int32_t moe_capacity(int64_t T, int32_t n_experts, int32_t top_k, double capacit
  * shared by calls that may run concurrently. */
 size_t moe_workspace_bytes(const moe_config* cfg);
 
-/* Prepare a workspace for first use: clears the latched device status (the
- * first 256 bytes).  Call once after allocating a workspace, before any other
+/* Prepare a workspace for first use: clears the latched device status and the
+ * kernels' arrival counters (the first 4352 bytes, or all of a smaller one).  Call once after allocating a workspace, before any other
  * entry point uses it; later calls keep it consistent by themselves.
  * Asynchronous on `stream`. */
 int32_t moe_workspace_init(void* ws, size_t ws_bytes, void* stream);

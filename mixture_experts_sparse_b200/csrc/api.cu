@@ -57,7 +57,7 @@ namespace {
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 struct Layout {
-    size_t hdr, part_cnt, part_psum, part_z, w_split, scan_state;
+    size_t hdr, w4_count, part_cnt, part_psum, part_z, w_split, scan_state;
     size_t idx, gate, pos, drop, counts, kept, offsets, f, P, aux;
     size_t row_token, row_gate, xe, h, ye;
     size_t prio_hist, prio_cursor, prio_list, prio_perm, prio_idx, prio_pos, prio_range;   // batch priority only
@@ -88,6 +88,7 @@ Layout layout_of(const moe_config& c) {
     L.rows = compact_rows(c);
     const size_t R = (size_t)(L.rows > 0 ? L.rows : 1);
     L.hdr = take(sizeof(WsHeader));
+    L.w4_count = take(4 * 2 * kW4Counters);
     const size_t nbr = (size_t)router_partial_rows(c.T, c.n_experts);
     L.part_cnt = take(4 * nbr * N);
     L.part_psum = take(4 * nbr * N);
@@ -227,7 +228,9 @@ size_t moe_workspace_bytes(const moe_config* cfg) {
 
 int32_t moe_workspace_init(void* ws, size_t ws_bytes, void* stream) {
     if (!ws || !aligned(ws) || ws_bytes < sizeof(WsHeader)) return MOE_ERR_WORKSPACE;
-    return cuda_status(cudaMemsetAsync(ws, 0, sizeof(WsHeader), (cudaStream_t)stream));
+    // the header and, in a layer workspace, the arrival counters behind it
+    const size_t clear = sizeof(WsHeader) + 4 * 2 * kW4Counters;
+    return cuda_status(cudaMemsetAsync(ws, 0, ws_bytes < clear ? ws_bytes : clear, (cudaStream_t)stream));
 }
 
 const char* moe_status_string(int32_t status) {
@@ -708,11 +711,15 @@ int32_t moe_expert_ffn(const moe_config* cfg, const void* xe, const int32_t* off
 
 static bool w4_group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
 
-// the layer workspace, then what H's rounding to bf16 left (h_lo)
+// the layer workspace, then what H's rounding to bf16 left (h_lo), then the sums
+// of tiles that CTAs share
 static size_t w4_lo_offset(const Layout& L) { return L.total; }
-static size_t w4_total(const moe_config& c, const Layout& L) {
+static size_t w4_part_offset(const moe_config& c, const Layout& L) {
     const size_t R = (size_t)(L.rows > 0 ? L.rows : 1);
     return L.total + round_up(2 * R * (size_t)c.d_ff, 256);
+}
+static size_t w4_total(const moe_config& c, const Layout& L) {
+    return w4_part_offset(c, L) + (size_t)w4_part_bytes();
 }
 
 size_t moe_w4_row_bytes(int64_t k) { return k < 0 ? 0 : (size_t)w4_row_bytes(k); }
@@ -756,6 +763,9 @@ struct W4Weights {
 
 static int32_t w4_check_weights(const moe_config* cfg, const W4Weights& w) {
     if (cfg->dtype != MOE_BF16 || !w4_group_ok(w.group)) return MOE_ERR_UNSUPPORTED;
+    // weight rows are 32-bit tensor-map coordinates
+    const int64_t widest = cfg->d_model > cfg->d_ff ? cfg->d_model : cfg->d_ff;
+    if (widest * cfg->n_experts >= (int64_t)1 << 31 || widest > (1 << 24)) return MOE_ERR_UNSUPPORTED;
     if (!req(w.q1) || !req(w.s1) || !req(w.q2) || !req(w.s2) || !opt(w.b1) || !opt(w.b3) || !opt(w.b2))
         return MOE_ERR_INVALID_ARG;
     if (cfg->act == MOE_SWIGLU ? (!req(w.q3) || !req(w.s3)) : (!opt(w.q3) || !opt(w.s3))) return MOE_ERR_INVALID_ARG;
@@ -784,6 +794,8 @@ static int32_t w4_ffn_impl(const moe_config* cfg, const W4Weights& w, const void
     a.h = at<__nv_bfloat16>(ws, L.h);
     a.h_lo = at<__nv_bfloat16>(ws, w4_lo_offset(L));
     a.ye = static_cast<__nv_bfloat16*>(ye);
+    a.part = at<float>(ws, w4_part_offset(*cfg, L));
+    a.count = at<int32_t>(ws, L.w4_count);
     a.hdr = at<WsHeader>(ws, L.hdr);
     return cuda_status(launch_w4_ffn(a, s));
 }

@@ -245,6 +245,8 @@ bool make_map_bf16_mn(CUtensorMap* map, const void* base, int64_t rows, int64_t 
 // driver rejects the view)
 bool make_map_bf16_mn_blocks(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t row_stride,
                              int box_rows, int blocks);
+// host: 2-D bytes [rows, pitch], box = box_rows x 128 bytes, 128-byte swizzle
+bool make_map_u8(CUtensorMap* map, const void* base, int64_t rows, int64_t pitch, int box_rows);
 // host: the same over the first `cols` columns of rows `row_stride` elements apart
 bool make_map_bf16_strided(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t row_stride,
                            int box_rows);

@@ -43,8 +43,13 @@ struct W4FfnArgs {
     __nv_bfloat16* h;      // [R_cap, d_ff]
     __nv_bfloat16* h_lo;   // [R_cap, d_ff]: what h's rounding left (few rows)
     __nv_bfloat16* ye;     // [R_cap, d]
+    float* part;           // w4_part_bytes(): sums of tiles that CTAs share
+    int32_t* count;        // [2][kW4Counters], zero between calls
     WsHeader* hdr;
 };
+constexpr int kW4GemvSmem = 72 * 1024;
+int w4_gemv_ctas(int sms);
+int64_t w4_part_bytes();
 cudaError_t launch_w4_quantize(int64_t mats, int64_t rows, int64_t k, int group, int dtype, const void* w, uint8_t* q,
                                uint16_t* scale, cudaStream_t s);
 cudaError_t launch_w4_dequantize(int64_t mats, int64_t rows, int64_t k, int group, int dtype, const uint8_t* q,

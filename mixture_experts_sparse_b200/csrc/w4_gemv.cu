@@ -1,31 +1,69 @@
-// Expert FFN on 4-bit weights for few rows per expert: matrix-vector work, bound
-// by the one read of the weights of every expert that has rows.
+// Expert FFN on 4-bit weights for few rows per expert: bound by the one read of
+// the weights of every expert that has rows.
 //
 //   stage 1: H = relu(x W1^T + b1), or silu(x W1^T + b1) * (x W3^T + b3)
 //   stage 2: y = H W2^T + b2              W[o][k] = q[o][k] s[o][k / G]
 //
-// A warp holds 16 output features and streams their packed rows from global
-// memory into registers, a block of 128 weights per row and step, D steps ahead;
-// the 16 bytes of a lane are, word by word, the A fragments of mma.sync m16n8k16
-// (w4.cuh), decoded to bf16 exactly as integers.  The tokens are the 8 columns,
-// so a tile is fed at one instruction per 2048 weights and eight tokens; what
-// bounds the loop is decoding (11 operations per 8 weights), still below the
-// rate at which HBM delivers them.  (A 128-row tcgen05 tile would be decoded
-// through shared memory or TMEM for the same few columns.)  The integer products
-// of a group are exact in the fp32 accumulator; the group's scale multiplies the
-// sum, once per row and group, in fp32.
-// The warps of a CTA take interleaved blocks of K and add their sums in order
-// through shared memory: no atomics, the same bits each time.
-// H keeps two bf16 parts, its rounding and the remainder (16 bits): the second
-// product costs one more mma per fragment, of which there are few, and the
-// output then has one rounding that matters.
+// A CTA has four consumer warps and a producer warp.  Its tile is 128 weight rows
+// (64 features of W1 and the same of W3 for SwiGLU) by up to 16 columns, a
+// pipeline stage 256 of K: the producer brings the packed rows with TMA
+// (128-byte swizzle) and the tokens' rows and the group scales with cp.async
+// into an mbarrier ring.  A consumer warp owns 32 weight rows as two m16n8k16
+// tiles; its 16-byte shared loads are, word by word, the A fragments (w4.cuh),
+// decoded to bf16 exactly as integers, so the products of a group are exact in
+// the fp32 accumulator and the group's scale multiplies their sum in fp32.
+// Lane g of an mma row group reads tile row perm(g): rows 0 4 1 5 2 6 3 7, whose
+// swizzled 16-byte chunks fall into different banks.
+// mma.sync and not tcgen05: with at most 16 tokens the tensor work is a few
+// per cent of either pipe, decoding and HBM bound the loop, and register
+// fragments save the way through shared memory or TMEM that a tcgen05 operand
+// takes.
+// H keeps two bf16 parts, its rounding and the remainder (16 bits in all): stage
+// 2 takes them as two columns per token, so the output has one rounding.
+//
+// The pipeline stages of all tiles form one list, cut into equal ranges, one per
+// CTA, so that every SM streams the same number of bytes whatever the sizes.  A
+// tile that two or more CTAs share is added up by the one that arrives last,
+// from fp32 parts in the workspace, in K order: the result depends on where the
+// cuts fall (on the live experts and rows), not on the order of arrival.
+#include "tc_common.cuh"
 #include "w4.cuh"
 
 namespace moe {
+using namespace tc;
 namespace {
 
-constexpr int kGemvWarps = 8;
-constexpr int kGemvThreads = 32 * kGemvWarps;
+constexpr int kWarps = 4;                        // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kRows = 32 * kWarps;               // weight rows of a tile
+constexpr int kStageBlocks = 2;                  // 128-weight blocks of K per stage
+constexpr int kStageK = kStageBlocks * kW4Block;
+constexpr int kWBytes = kRows * kStageBlocks * kW4BlockBytes;   // 16 KB
+constexpr int kXBytes = 8 * kStageK * 2;         // per 8 columns
+constexpr int kOutPitch = kRows + 4;             // conflict-free accumulator writes
+constexpr int kMaxStages = 8;
+constexpr int kCtasPerSm = 3;
+constexpr int kMinSteps = 2;                     // stages per CTA at least
+constexpr int kPartFloats = 16 * kRows;          // one fp32 part of a tile
+
+enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
+
+struct GemvParams {
+    const int32_t* offsets; int N; int64_t R_cap;
+    int m_dim;                    // output features
+    int k_dim;
+    const uint16_t* sa; const uint16_t* sb;              // scales (sb: W3)
+    const __nv_bfloat16* bias_a; const __nv_bfloat16* bias_b;
+    const __nv_bfloat16* x; const __nv_bfloat16* x_lo;   // [R, k_dim]
+    __nv_bfloat16* out; __nv_bfloat16* out_lo;           // [R, m_dim]
+    float* part;                  // [CTAs][2][kPartFloats]
+    int32_t* count;               // [CTAs] arrivals per shared tile, zero between calls
+    int32_t* clear;               // [clear_n] the other stage's counters
+    int clear_n;
+    int smem_bytes;               // dynamic shared memory of a CTA
+    int32_t* status;
+    long long limit_ns;
+};
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -36,265 +74,498 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+// 16 bytes global -> shared; ok = false fills zeros
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+// arrive on the barrier when this thread's copies so far have landed
+__device__ __forceinline__ void cp_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
     return v;
 }
-
-struct GemvParams {
-    const int32_t* offsets; int N; int64_t R_cap;
-    int m_dim;                    // output features
-    int k_dim;
-    W4Mat wa, wb;                 // wb: W3 (SwiGLU stage 1)
-    const __nv_bfloat16* bias_a; const __nv_bfloat16* bias_b;
-    const __nv_bfloat16* x; const __nv_bfloat16* x_lo;   // [R, k_dim]
-    __nv_bfloat16* out; __nv_bfloat16* out_lo;           // [R, m_dim]
-};
-
-enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
-
-// MATS: weight matrices (2: SwiGLU).  One step: 16 rows x 128 weights of each.
-template <int MATS>
-struct Step {
-    uint4 w[MATS][2];        // rows g and g + 8, this lane's 16 bytes
-    uint16_t s[MATS][2];     // scales of the group that holds word `t` of the block
-};
-
-template <int MATS, int G>
-__device__ __forceinline__ void load_step(Step<MATS>& st, const uint8_t* const (&q)[MATS], const uint16_t* const (&s)[MATS],
-                                          int64_t pitch, int m_dim, int kb, int nb, int ng, int t) {
-    if (kb < nb) {
-        const int g = min(kb * (kW4Block / G) + t * (kW4Block / G) / 4, ng - 1);   // past the last group: zero weights
-#pragma unroll
-        for (int i = 0; i < MATS; ++i) {
-            st.w[i][0] = ldg_stream(q[i] + kb * kW4BlockBytes);
-            st.w[i][1] = ldg_stream(q[i] + 8 * pitch + kb * kW4BlockBytes);
-            st.s[i][0] = __ldg(s[i] + (int64_t)g * m_dim);
-            st.s[i][1] = __ldg(s[i] + (int64_t)g * m_dim + 8);
-        }
-    }
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
+    return __uint_as_float((uint32_t)v << 16);
 }
-
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
-// Rows [row0, row0 + n) of x times 16 features: acc += this warp's blocks of K.
-template <int EPI, int G, int NT>
-__device__ __forceinline__ void gemv_unit(const GemvParams& p, int e, int m0, int64_t row0, int n, float* s_red) {
-    constexpr int MATS = EPI == W4_SWIGLU ? 2 : 1;
-    constexpr bool HILO = EPI == W4_OUT;
-    constexpr int D = NT == 1 ? (MATS == 2 ? 4 : 6) : 3;   // steps in flight
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int nb = (p.k_dim + kW4Block - 1) / kW4Block, ng = (p.k_dim + G - 1) / G;
-    const int64_t pitch = (int64_t)nb * kW4BlockBytes;
-    const uint8_t* q[MATS];
-    const uint16_t* s[MATS];
-#pragma unroll
-    for (int i = 0; i < MATS; ++i) {
-        const W4Mat& m = i == 0 ? p.wa : p.wb;
-        q[i] = m.q + ((int64_t)e * p.m_dim + m0 + g) * pitch + 16 * t;
-        s[i] = m.s + (int64_t)e * ng * p.m_dim + m0 + g;
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    int row[129];
+    int exp[128];      // live experts
+    int first[129];    // their first unit
+    int live, abort, last;
+};
+
+// The list of a launch: units (live expert, feature tile, row chunk), each of
+// `steps` pipeline stages.
+struct Plan {
+    int tiles, steps, chunk;   // feature tiles; stages per unit; rows per chunk
+    int64_t units, total;      // total = units * steps
+    int ctas;
+    __device__ int64_t begin(int c) const { return total * c / ctas; }
+    __device__ int cta_of(int64_t step) const { return (int)(((step + 1) * ctas - 1) / total); }
+};
+
+struct Unit {
+    int e, m0, row0, n;
+};
+
+__device__ __forceinline__ Unit unit_of(const Shared& sh, const Plan& pl, int64_t u, int feats) {
+    int lo = 0, hi = sh.live;   // first[lo] <= u < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.first[mid] <= u) lo = mid;
+        else hi = mid;
     }
-    float acc[MATS][NT][4];
+    const int e = sh.exp[lo], local = (int)(u - sh.first[lo]);
+    const int chunks = (sh.row[e + 1] - sh.row[e] + pl.chunk - 1) / pl.chunk;
+    Unit t;   // the chunks of a feature tile follow one another: its weights are in L2
+    t.e = e;
+    t.m0 = local / chunks * feats;
+    t.row0 = sh.row[e] + local % chunks * pl.chunk;
+    t.n = min(pl.chunk, sh.row[e + 1] - t.row0);
+    return t;
+}
+
+// A position in the list.
+struct Cursor {
+    int64_t u;
+    int ks;
+    Unit t;
+    __device__ void start(const Shared& sh, const Plan& pl, int64_t step, int feats) {
+        u = step / pl.steps;
+        ks = (int)(step - u * pl.steps);
+        t = unit_of(sh, pl, u, feats);
+    }
+    __device__ void next(const Shared& sh, const Plan& pl, int feats) {
+        if (++ks < pl.steps) return;
+        ks = 0;
+        if (++u < pl.units) t = unit_of(sh, pl, u, feats);
+    }
+};
+
+template <int EPI, int G, int NT>
+struct Shape {
+    static constexpr int MATS = EPI == W4_SWIGLU ? 2 : 1;
+    static constexpr int FEATS = kRows / MATS;                   // output features of a tile
+    static constexpr bool HILO = EPI == W4_OUT;
+    static constexpr int CHUNK = HILO ? 4 * NT : 8 * NT;         // tokens of a tile (two columns each with HILO)
+    static constexpr int SGROUPS = kStageK / G;                  // groups per stage
+    static constexpr int X_OFF = kWBytes;
+    static constexpr int S_OFF = X_OFF + NT * kXBytes;
+    static constexpr int STAGE = (S_OFF + SGROUPS * kRows * 2 + 1023) / 1024 * 1024;
+    static constexpr int OUT_BYTES = CHUNK * kOutPitch * 4;
+};
+
+template <int EPI, int G, int NT>
+__device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* ma, const CUtensorMap* mb, Shared& sh,
+                                        uint32_t ring, int stages, const Plan& pl, const Waiter& w) {
+    using S = Shape<EPI, G, NT>;
+    const int lane = threadIdx.x & 31;
+    const int ng = (p.k_dim + G - 1) / G;
+    // the rows of x and the scales of the stage at c
+    auto rows_of = [&](const Cursor& c, int st) {
+        const int k0 = c.ks * kStageK;
+        const uint32_t base = ring + st * S::STAGE;
+        const int k = k0 + 8 * lane;          // this lane's 8 of the row's 256
+        const uint32_t xd = base + S::X_OFF + (lane >> 2) * (8 * NT * 64) + (lane & 3) * 16;
+        const bool in = k < p.k_dim;
+        int64_t at = (int64_t)c.t.row0 * p.k_dim + (in ? k : 0);
+        for (int v = 0; v < c.t.n; ++v, at += p.k_dim) {
+            cp16(xd + v * 64, p.x + at, in);
+            if (S::HILO) cp16(xd + (4 * NT + v) * 64, p.x_lo + at, in);
+        }
+        // scales: 16 lanes a group, 8 tile rows a lane
+        const int r = (lane & 15) * 8;        // tile row
+        const uint16_t* sc = S::MATS == 2 && r >= S::FEATS ? p.sb : p.sa;
+        const int f = c.t.m0 + (S::MATS == 2 ? r % S::FEATS : r);
 #pragma unroll
-    for (int i = 0; i < MATS; ++i)
+        for (int i = 0; i < S::SGROUPS; i += 2) {
+            const int gi = i + (lane >> 4), g = k0 / G + gi;
+            const bool have = g < ng && f < p.m_dim;
+            cp16(base + S::S_OFF + gi * kRows * 2 + r * 2, have ? sc + ((int64_t)c.t.e * ng + g) * p.m_dim + f : p.sa, have);
+        }
+        cp_arrive(smem_u32(&sh.full[st]));
+    };
+    const int64_t begin = pl.begin(blockIdx.x), end = pl.begin(blockIdx.x + 1);
+    Cursor cur;
+    cur.start(sh, pl, begin, S::FEATS);
+    Cursor late = cur;               // stage 2: the first stages' rows, asked for after the wait
+    int pending = 0, stage = 0;
+    bool waited = EPI != W4_OUT, ok = true;
+    auto catch_up = [&]() {
+        pdl_wait();
+        waited = true;
+        for (int i = 0; i < pending; ++i) {
+            rows_of(late, i);
+            late.next(sh, pl, S::FEATS);
+        }
+    };
+    uint32_t phase = 0, used = 0;
+    for (int64_t step = begin; step < end; ++step) {
+        if (!waited && pending == stages) catch_up();   // the ring is full of weights
+        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.empty[stage]), phase ^ 1u, w));
+        if (!ok) break;
+        if (lane == 0) {
+            const int kb = cur.ks * kStageBlocks * kW4BlockBytes;
+            const uint32_t fb = smem_u32(&sh.full[stage]), base = ring + stage * S::STAGE;
+            const int row = cur.t.e * p.m_dim + cur.t.m0;
+            const bool second = S::MATS == 2 || cur.t.m0 + 64 < p.m_dim;   // the upper 64 rows hold something
+            mbar_expect_tx(fb, second ? kWBytes : kWBytes / 2);
+            tma_load_2d(base, ma, fb, kb, row);
+            if (second) tma_load_2d(base + kWBytes / 2, S::MATS == 2 ? mb : ma, fb, kb, S::MATS == 2 ? row : row + 64);
+        }
+        __syncwarp();
+        used |= 1u << stage;
+        if (waited) rows_of(cur, stage);
+        else ++pending;
+        cur.next(sh, pl, S::FEATS);
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    if (!waited) catch_up();
+    // nothing of this warp's copies is in flight when the CTA ends
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok && lane == 0) {   // aborted: the weights asked for last have landed too
+        for (int s = 0; s < stages; ++s)
+            if (used >> s & 1u)
+                drain_bar(smem_u32(&sh.full[s]), s < stage ? phase : phase ^ 1u, p.limit_ns, p.status);
+    }
+    __syncwarp();
+}
+
+template <int EPI, int G, int NT>
+__device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, uint32_t ring, float* s_out, int stages,
+                                        const Plan& pl, const Waiter& w) {
+    using S = Shape<EPI, G, NT>;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int nb = (p.k_dim + kW4Block - 1) / kW4Block, ng = (p.k_dim + G - 1) / G;
+    const int pg = (g >> 1) | ((g & 1) << 2);   // tile row of mma row g: 0 4 1 5 2 6 3 7
+    // m16 tile i of this warp: SwiGLU, the same 16 features of either matrix; else 32 rows
+    auto tile_row = [&](int i) { return S::MATS == 2 ? i * S::FEATS + 16 * warp : 32 * warp + 16 * i; };
+    int stage = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+    int64_t step = pl.begin(blockIdx.x);
+    const int64_t end = pl.begin(blockIdx.x + 1);
+    while (step < end) {
+        const int64_t u = step / pl.steps, u0 = u * pl.steps, u1 = u0 + pl.steps;
+        const int64_t stop = min(end, u1);
+        const Unit un = unit_of(sh, pl, u, S::FEATS);
+        float acc[2][NT][4];
 #pragma unroll
-        for (int c = 0; c < NT; ++c)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][c][j] = 0.f;
-    Step<MATS> ring[D];
+            for (int c = 0; c < NT; ++c)
 #pragma unroll
-    for (int i = 0; i < D; ++i) load_step<MATS, G>(ring[i], q, s, pitch, p.m_dim, warp + i * kGemvWarps, nb, ng, t);
-    const __nv_bfloat16* xr = p.x + (row0 + g) * p.k_dim + 8 * t;
-    const __nv_bfloat16* xl = HILO ? p.x_lo + (row0 + g) * p.k_dim + 8 * t : nullptr;
-    for (int base = warp; base < nb; base += D * kGemvWarps) {
+                for (int r = 0; r < 4; ++r) acc[i][c][r] = 0.f;
+        const int64_t from = step;
+        for (; step < stop; ++step) {
+            // after an abort the warp only keeps the barriers going
+            if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(smem_u32(&sh.full[stage]), phase, w));
+            const uint32_t base = ring + stage * S::STAGE;
+            const int kb0 = (int)(step - u0) * kStageBlocks;
 #pragma unroll
-        for (int i = 0; i < D; ++i) {
-            const int kb = base + i * kGemvWarps;
-            if (kb < nb) {
-                Step<MATS>& st = ring[i];
-                float part[MATS][NT][4];
+            for (int b = 0; b < kStageBlocks; ++b) {
+                if (dead || kb0 + b >= nb) break;   // a block past K holds nothing
+                uint4 wd[2][2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        wd[i][h] = lds16(base + (tile_row(i) + 8 * h + pg) * 128 + (((4 * b + t) ^ pg) << 4));
+                float part[2][NT][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if ((j * (kW4Block / G)) % 4 == 0) {   // word j starts a group
 #pragma unroll
-                        for (int m = 0; m < MATS; ++m)
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
                             for (int c = 0; c < NT; ++c)
 #pragma unroll
-                                for (int r = 0; r < 4; ++r) part[m][c][r] = 0.f;
+                                for (int r = 0; r < 4; ++r) part[i][c][r] = 0.f;
                     }
-                    const int k0 = kb * kW4Block + 32 * j;
-                    uint4 b[NT], bl[HILO ? NT : 1];
+                    uint4 x[NT];
 #pragma unroll
                     for (int c = 0; c < NT; ++c) {
-                        const bool ok = 8 * c + g < n && k0 + 8 * t < p.k_dim;
-                        b[c] = ok ? __ldg(reinterpret_cast<const uint4*>(xr + (int64_t)8 * c * p.k_dim + k0))
-                                  : make_uint4(0, 0, 0, 0);
-                        if (HILO)
-                            bl[c] = ok ? __ldg(reinterpret_cast<const uint4*>(xl + (int64_t)8 * c * p.k_dim + k0))
-                                       : make_uint4(0, 0, 0, 0);
+                        const int v = 8 * c + g;
+                        const bool ok = (S::HILO ? v % (4 * NT) : v) < un.n;
+                        x[c] = make_uint4(0, 0, 0, 0);
+                        if (ok) x[c] = lds16(base + S::X_OFF + ((4 * b + j) * 8 * NT + v) * 64 + t * 16);
                     }
 #pragma unroll
-                    for (int m = 0; m < MATS; ++m) {
-                        const uint32_t w0 = word_of(st.w[m][0], j), w1 = word_of(st.w[m][1], j);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t w0 = word_of(wd[i][0], j), w1 = word_of(wd[i][1], j);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint32_t a0 = w4_pair(w0, 2 * h), a1 = w4_pair(w1, 2 * h);
                             const uint32_t a2 = w4_pair(w0, 2 * h + 1), a3 = w4_pair(w1, 2 * h + 1);
 #pragma unroll
-                            for (int c = 0; c < NT; ++c) {
-                                mma16816(part[m][c], a0, a1, a2, a3, h ? b[c].z : b[c].x, h ? b[c].w : b[c].y);
-                                if (HILO)
-                                    mma16816(part[m][c], a0, a1, a2, a3, h ? bl[c].z : bl[c].x, h ? bl[c].w : bl[c].y);
-                            }
+                            for (int c = 0; c < NT; ++c)
+                                mma16816(part[i][c], a0, a1, a2, a3, h ? x[c].z : x[c].x, h ? x[c].w : x[c].y);
                         }
                     }
                     if (((j + 1) * (kW4Block / G)) % 4 == 0) {   // word j ends a group
+                        const int gi = b * (kW4Block / G) + j * (kW4Block / G) / 4;   // group of the stage
+                        const bool have = (kb0 * (kW4Block / G) + gi) < ng;
 #pragma unroll
-                        for (int m = 0; m < MATS; ++m) {
-                            uint32_t u0 = st.s[m][0], u1 = st.s[m][1];
-                            if (G < kW4Block) {   // the lane of the quad that loaded this group's scale
-                                u0 = __shfl_sync(0xffffffffu, u0, (lane & ~3) | j);
-                                u1 = __shfl_sync(0xffffffffu, u1, (lane & ~3) | j);
-                            }
-                            const float f0 = __uint_as_float(u0 << 16), f1 = __uint_as_float(u1 << 16);
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t sa = base + S::S_OFF + (gi * kRows + tile_row(i) + pg) * 2;
+                            const float f0 = lds_bf16(sa), f1 = lds_bf16(sa + 16);
+                            if (have) {   // past the last group all weights are 0
 #pragma unroll
-                            for (int c = 0; c < NT; ++c) {
-                                acc[m][c][0] = fmaf(part[m][c][0], f0, acc[m][c][0]);
-                                acc[m][c][1] = fmaf(part[m][c][1], f0, acc[m][c][1]);
-                                acc[m][c][2] = fmaf(part[m][c][2], f1, acc[m][c][2]);
-                                acc[m][c][3] = fmaf(part[m][c][3], f1, acc[m][c][3]);
+                                for (int c = 0; c < NT; ++c) {
+                                    acc[i][c][0] = fmaf(part[i][c][0], f0, acc[i][c][0]);
+                                    acc[i][c][1] = fmaf(part[i][c][1], f0, acc[i][c][1]);
+                                    acc[i][c][2] = fmaf(part[i][c][2], f1, acc[i][c][2]);
+                                    acc[i][c][3] = fmaf(part[i][c][3], f1, acc[i][c][3]);
+                                }
                             }
                         }
                     }
                 }
-                load_step<MATS, G>(st, q, s, pitch, p.m_dim, kb + D * kGemvWarps, nb, ng, t);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+        // accumulators -> s_out[token][tile row]
+        named_bar(1, kRows);   // the previous tile's values have been read
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (S::HILO) {   // a token's two columns: column v and v + 4 NT
+#pragma unroll
+                for (int c = 0; c < (NT + 1) / 2; ++c)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][c][r] += NT == 1 ? __shfl_down_sync(0xffffffffu, acc[i][c][r], 2) : acc[i][c + NT / 2][r];
+            }
+#pragma unroll
+            for (int c = 0; c < (S::HILO ? (NT + 1) / 2 : NT); ++c)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int col = 8 * c + 2 * t + (r & 1);
+                    if (col < S::CHUNK) s_out[col * kOutPitch + tile_row(i) + pg + 8 * (r >> 1)] = acc[i][c][r];
+                }
+        }
+        named_bar(1, kRows);
+        if (from > u0 || stop < u1) {   // other CTAs hold the rest of the tile's K
+            const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u1 - 1);
+            float* dst = p.part + ((int64_t)blockIdx.x * 2 + (from > u0 ? 0 : 1)) * kPartFloats;
+            for (int col = 0; col < un.n; ++col) __stcg(dst + col * kRows + tid, s_out[col * kOutPitch + tid]);
+            __threadfence();
+            named_bar(1, kRows);
+            if (tid == 0) {
+                const int before = atomicAdd(p.count + c0, 1);
+                sh.last = before == c1 - c0;
+                if (before == c1 - c0) p.count[c0] = 0;
+            }
+            named_bar(1, kRows);
+            if (!sh.last) continue;
+            __threadfence();
+            for (int col = 0; col < un.n; ++col) {
+                float v = 0.f;
+                for (int c = c0; c <= c1; ++c)   // K order
+                    v += __ldcg(p.part + ((int64_t)c * 2 + (pl.begin(c) > u0 ? 0 : 1)) * kPartFloats + col * kRows + tid);
+                s_out[col * kOutPitch + tid] = v;
+            }
+            named_bar(1, kRows);
+        }
+        // bias, activation, output: a thread per feature, the columns dealt to the tile's MATS halves
+        const int f = tid % S::FEATS, feat = un.m0 + f;
+        if (feat < p.m_dim) {
+            const int64_t bi = (int64_t)un.e * p.m_dim + feat;
+            const float ba = p.bias_a ? __bfloat162float(p.bias_a[bi]) : 0.f;
+            const float bb = S::MATS == 2 && p.bias_b ? __bfloat162float(p.bias_b[bi]) : 0.f;
+            for (int col = tid / S::FEATS; col < un.n; col += S::MATS) {
+                float o = s_out[col * kOutPitch + f] + ba;
+                if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
+                if (EPI == W4_SWIGLU)
+                    o = o / (1.f + fast_exp2(-o * kLog2e)) * (s_out[col * kOutPitch + S::FEATS + f] + bb);
+                const __nv_bfloat16 hi = __float2bfloat16_rn(o);
+                const int64_t at = (int64_t)(un.row0 + col) * p.m_dim + feat;
+                p.out[at] = hi;
+                if (EPI != W4_OUT) p.out_lo[at] = __float2bfloat16_rn(o - __bfloat162float(hi));
             }
         }
     }
-    // warps in order: s_red[warp][matrix][column][feature]
-    constexpr int TILE = 16 * 8 * NT;
-#pragma unroll
-    for (int m = 0; m < MATS; ++m)
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                s_red[(warp * MATS + m) * TILE + (8 * c + 2 * t + (r & 1)) * 16 + g + 8 * (r >> 1)] = acc[m][c][r];
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * n; i += kGemvThreads) {
-        const int col = i >> 4, f = i & 15, feat = m0 + f;
-        float v[MATS];
-#pragma unroll
-        for (int m = 0; m < MATS; ++m) {
-            v[m] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kGemvWarps; ++w) v[m] += s_red[(w * MATS + m) * TILE + col * 16 + f];
+}
+
+template <int EPI, int G, int NT>
+__device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap* ma, const CUtensorMap* mb, Shared& sh,
+                                          uint8_t* smem) {
+    using S = Shape<EPI, G, NT>;
+    const int tid = threadIdx.x;
+    Plan pl;
+    pl.chunk = S::CHUNK;
+    pl.tiles = (p.m_dim + S::FEATS - 1) / S::FEATS;
+    pl.steps = (p.k_dim + kStageK - 1) / kStageK;
+    if (tid == 0) {   // live experts and their first units
+        int c = 0, u = 0;
+        for (int e = 0; e < p.N; ++e) {
+            const int n = sh.row[e + 1] - sh.row[e];
+            if (n <= 0) continue;
+            sh.exp[c] = e;
+            sh.first[c++] = u;
+            u += (n + S::CHUNK - 1) / S::CHUNK * pl.tiles;
         }
-        const __nv_bfloat16* ba = p.bias_a ? p.bias_a + (int64_t)e * p.m_dim + feat : nullptr;
-        if (ba) v[0] += __bfloat162float(*ba);
-        float o = v[0];
-        if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
-        if (EPI == W4_SWIGLU) {
-            if (p.bias_b) v[MATS - 1] += __bfloat162float(p.bias_b[(int64_t)e * p.m_dim + feat]);
-            o = o / (1.f + fast_exp2(-o * kLog2e)) * v[MATS - 1];
-        }
-        const __nv_bfloat16 hi = __float2bfloat16_rn(o);
-        p.out[(row0 + col) * p.m_dim + feat] = hi;
-        if (EPI != W4_OUT) p.out_lo[(row0 + col) * p.m_dim + feat] = __float2bfloat16_rn(o - __bfloat162float(hi));
+        sh.first[c] = u;
+        sh.live = c;
     }
     __syncthreads();
+    pl.units = sh.first[sh.live];
+    pl.total = pl.units * pl.steps;
+    const int64_t most = (pl.total + kMinSteps - 1) / kMinSteps;
+    pl.ctas = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
+    if ((int)blockIdx.x >= pl.ctas) {
+        pdl_wait();
+        pdl_launch();
+        return;
+    }
+    const int stages = min(kMaxStages, (p.smem_bytes - 1024 - S::OUT_BYTES) / S::STAGE);
+    float* s_out = reinterpret_cast<float*>(smem + stages * S::STAGE);
+    const Waiter w{&sh.abort, p.status, p.limit_ns};
+    if (tid >= 32 * kWarps) {
+        produce<EPI, G, NT>(p, ma, mb, sh, smem_u32(smem), stages, pl, w);
+    } else {
+        if (EPI == W4_OUT) {
+            pdl_wait();
+            pdl_launch();
+        }
+        consume<EPI, G, NT>(p, sh, smem_u32(smem), s_out, stages, pl, w);
+    }
 }
 
 template <int EPI, int G>
-__global__ void __launch_bounds__(kGemvThreads, 2)
-w4_gemv_kernel(const GemvParams p) {
-    constexpr int MATS = EPI == W4_SWIGLU ? 2 : 1;
-    __shared__ float s_red[kGemvWarps * MATS * 16 * 16];
-    __shared__ int s_row[129], s_exp[128], s_live;
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemvParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ __align__(8) Shared sh;
+    __shared__ int s_most;
     const int tid = threadIdx.x;
+    if (tid == 0) {
+        for (int s = 0; s < kMaxStages; ++s) {
+            mbar_init(smem_u32(&sh.full[s]), 1 + 32);     // the TMA's expect and the producer lanes' copies
+            mbar_init(smem_u32(&sh.empty[s]), kWarps);
+        }
+        sh.abort = 0;
+        s_most = 0;
+        mbar_fence_init();
+        prefetch_tmap(&map_a);
+        prefetch_tmap(&map_b);
+    }
+    // Stage 2 may start while stage 1 drains: the offsets and the weights are
+    // inputs of both, so stage 2 reads them before it waits for stage 1's rows.
     if (EPI != W4_OUT) {
         pdl_wait();
         pdl_launch();
     }
-    // Stage 2 starts while stage 1 drains: the offsets are inputs of both, so they
-    // are read before the wait.
-    for (int i = tid; i <= p.N; i += kGemvThreads) {
+    for (int i = tid; i <= p.N; i += kThreads) {
         const int64_t v = p.offsets[i];
-        s_row[i] = (int)(v < 0 ? 0 : (v > p.R_cap ? p.R_cap : v));
+        sh.row[i] = (int)(v < 0 ? 0 : (v > p.R_cap ? p.R_cap : v));
     }
     __syncthreads();
-    if (tid == 0) {
-        int c = 0;
-        for (int e = 0; e < p.N; ++e)
-            if (s_row[e + 1] > s_row[e]) s_exp[c++] = e;
-        s_live = c;
-    }
+    for (int i = tid; i < p.N; i += kThreads) atomicMax(&s_most, sh.row[i + 1] - sh.row[i]);
     __syncthreads();
-    if (EPI == W4_OUT) {
+    const int most = s_most;
+    if (most > 0) {
+        if (most <= (EPI == W4_OUT ? 4 : 8)) run_tiles<EPI, G, 1>(p, &map_a, &map_b, sh, smem);
+        else run_tiles<EPI, G, 2>(p, &map_a, &map_b, sh, smem);
+    } else {
         pdl_wait();
         pdl_launch();
     }
-    const int tiles = p.m_dim / 16;
-    const int64_t units = (int64_t)s_live * tiles;
-    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-        const int e = s_exp[u / tiles], m0 = (int)(u % tiles) * 16;
-        const int r1 = s_row[e + 1];
-        for (int r = s_row[e]; r < r1;) {
-            const int left = r1 - r;
-            if (left <= 8) {
-                gemv_unit<EPI, G, 1>(p, e, m0, r, left, s_red);
-                r += 8;
-            } else {
-                gemv_unit<EPI, G, 2>(p, e, m0, r, min(left, 16), s_red);
-                r += 16;
-            }
-        }
-    }
+    // The other stage's counters: stage 1 clears stage 2's, which starts after
+    // it, and stage 2 (past its wait) those of the next call's stage 1.
+    if (blockIdx.x == 0)
+        for (int i = tid; i < p.clear_n; i += kThreads) p.clear[i] = 0;
+}
+
+// packed rows [rows][pitch] bytes: boxes of 64 rows x 128 bytes, 128-byte swizzle
+bool make_map_w4(CUtensorMap* map, const void* q, int64_t rows, int64_t pitch) {
+    return make_map_u8(map, q, rows, pitch, 64);
+}
+
+template <int EPI, int G>
+cudaError_t run_gemv_g(const CUtensorMap& a, const CUtensorMap& b, GemvParams p, int sms, cudaStream_t s) {
+    auto kern = w4_gemv_kernel<EPI, G>;
+    cudaError_t err = once_per_device(reinterpret_cast<const void*>(kern), [](const void* k) {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4GemvSmem);
+    });
+    if (err != cudaSuccess) return err;
+    p.smem_bytes = kW4GemvSmem;
+    return launch_k(kern, dim3((unsigned)w4_gemv_ctas(sms)), dim3(kThreads), kW4GemvSmem, s, 1, a, b, p);
 }
 
 template <int EPI>
-cudaError_t run_gemv(const GemvParams& p, int group, int sms, cudaStream_t s) {
-    const dim3 grid((unsigned)(2 * sms)), block(kGemvThreads);
-    if (group == 32) return launch_k(w4_gemv_kernel<EPI, 32>, grid, block, 0, s, 1, p);
-    if (group == 64) return launch_k(w4_gemv_kernel<EPI, 64>, grid, block, 0, s, 1, p);
-    return launch_k(w4_gemv_kernel<EPI, 128>, grid, block, 0, s, 1, p);
+cudaError_t run_gemv(const CUtensorMap& a, const CUtensorMap& b, const GemvParams& p, int group, int sms, cudaStream_t s) {
+    if (group == 32) return run_gemv_g<EPI, 32>(a, b, p, sms, s);
+    if (group == 64) return run_gemv_g<EPI, 64>(a, b, p, sms, s);
+    return run_gemv_g<EPI, 128>(a, b, p, sms, s);
 }
 
 }  // namespace
+
+int w4_gemv_ctas(int sms) { return sms * kCtasPerSm < kW4Counters ? sms * kCtasPerSm : kW4Counters; }
+int64_t w4_part_bytes() { return (int64_t)kW4Counters * 2 * kPartFloats * 4; }
 
 cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     int sms = 0;
     cudaError_t err = device_sm_count(&sms);
     if (err != cudaSuccess) return err;
+    CUtensorMap m1, m3, m2;
+    if (!make_map_w4(&m1, a.w1.q, (int64_t)a.N * a.d_ff, w4_row_bytes(a.d)) ||
+        !make_map_w4(&m2, a.w2.q, (int64_t)a.N * a.d, w4_row_bytes(a.d_ff)))
+        return cudaErrorInvalidValue;
+    m3 = m1;
+    if (a.act == MOE_SWIGLU && !make_map_w4(&m3, a.w3.q, (int64_t)a.N * a.d_ff, w4_row_bytes(a.d)))
+        return cudaErrorInvalidValue;
     GemvParams p{};
     p.offsets = a.offsets;
     p.N = a.N;
     p.R_cap = a.R_cap;
+    p.part = a.part;
+    p.status = &a.hdr->status;
+    p.limit_ns = kWaitLimitNs;
+    p.clear_n = w4_gemv_ctas(sms);
     p.m_dim = a.d_ff;
     p.k_dim = a.d;
-    p.wa = a.w1;
-    p.wb = a.w3;
+    p.sa = a.w1.s;
+    p.sb = a.w3.s;
     p.bias_a = a.b1;
     p.bias_b = a.b3;
     p.x = a.xe;
     p.out = a.h;
     p.out_lo = a.h_lo;
-    err = a.act == MOE_SWIGLU ? run_gemv<W4_SWIGLU>(p, a.group, sms, s) : run_gemv<W4_RELU>(p, a.group, sms, s);
+    p.count = a.count;
+    p.clear = a.count + kW4Counters;
+    err = a.act == MOE_SWIGLU ? run_gemv<W4_SWIGLU>(m1, m3, p, a.group, sms, s)
+                              : run_gemv<W4_RELU>(m1, m3, p, a.group, sms, s);
     if (err != cudaSuccess) return err;
     p.m_dim = a.d;
     p.k_dim = a.d_ff;
-    p.wa = a.w2;
+    p.sa = a.w2.s;
     p.bias_a = a.b2;
     p.bias_b = nullptr;
     p.x = a.h;
     p.x_lo = a.h_lo;
     p.out = a.ye;
     p.out_lo = nullptr;
-    return run_gemv<W4_OUT>(p, a.group, sms, s);
+    p.count = a.count + kW4Counters;
+    p.clear = a.count;
+    return run_gemv<W4_OUT>(m2, m2, p, a.group, sms, s);
 }
 
 }  // namespace moe
