@@ -29,7 +29,8 @@ struct W4Mat {            // one weight matrix per expert: [N][rows][K]
 // Weights 2 p and 2 p + 1 of the word's eight as a bf16 pair: 128 + (q + 8) is
 // exact in bf16 (0x4300 is 128, whose last place is 1), and so is the difference.
 __device__ __forceinline__ uint32_t w4_pair(uint32_t w, int p) {
-    const uint32_t u = ((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t u;   // (w >> 4 p & mask) | magic in one operation (two immediates would make it two)
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
     const uint32_t c = 0x43084308u;   // 136, 136
     __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&c));
     return *reinterpret_cast<uint32_t*>(&r);

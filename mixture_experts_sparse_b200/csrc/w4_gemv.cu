@@ -67,11 +67,19 @@ struct GemvParams {
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// the first product of a group: c = a b
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // 16 bytes global -> shared; ok = false fills zeros
@@ -82,15 +90,10 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
 __device__ __forceinline__ void cp_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-    return v;
-}
-__device__ __forceinline__ float lds_bf16(uint32_t addr) {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr));
-    return __uint_as_float((uint32_t)v << 16);
+// plain loads, so that the compiler moves them ahead of the mma they feed
+__device__ __forceinline__ uint4 lds16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ float lds_bf16(const uint8_t* p) {
+    return __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16);
 }
 __device__ __forceinline__ uint32_t word_of(const uint4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 
@@ -243,7 +246,7 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
 }
 
 template <int EPI, int G, int NT>
-__device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, uint32_t ring, float* s_out, int stages,
+__device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const uint8_t* ring, float* s_out, int stages,
                                         const Plan& pl, const Waiter& w) {
     using S = Shape<EPI, G, NT>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -271,7 +274,7 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, uint32_
         for (; step < stop; ++step) {
             // after an abort the warp only keeps the barriers going
             if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(smem_u32(&sh.full[stage]), phase, w));
-            const uint32_t base = ring + stage * S::STAGE;
+            const uint8_t* base = ring + stage * S::STAGE;
             const int kb0 = (int)(step - u0) * kStageBlocks;
 #pragma unroll
             for (int b = 0; b < kStageBlocks; ++b) {
@@ -285,22 +288,11 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, uint32_
                 float part[2][NT][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if ((j * (kW4Block / G)) % 4 == 0) {   // word j starts a group
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-#pragma unroll
-                            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) part[i][c][r] = 0.f;
-                    }
+                    const bool first = (j * (kW4Block / G)) % 4 == 0;   // word j starts a group
                     uint4 x[NT];
 #pragma unroll
-                    for (int c = 0; c < NT; ++c) {
-                        const int v = 8 * c + g;
-                        const bool ok = (S::HILO ? v % (4 * NT) : v) < un.n;
-                        x[c] = make_uint4(0, 0, 0, 0);
-                        if (ok) x[c] = lds16(base + S::X_OFF + ((4 * b + j) * 8 * NT + v) * 64 + t * 16);
-                    }
+                    for (int c = 0; c < NT; ++c)   // a column that no token fills holds anything: it is not read back
+                        x[c] = lds16(base + S::X_OFF + ((4 * b + j) * 8 * NT + 8 * c + g) * 64 + t * 16);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const uint32_t w0 = word_of(wd[i][0], j), w1 = word_of(wd[i][1], j);
@@ -309,8 +301,11 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, uint32_
                             const uint32_t a0 = w4_pair(w0, 2 * h), a1 = w4_pair(w1, 2 * h);
                             const uint32_t a2 = w4_pair(w0, 2 * h + 1), a3 = w4_pair(w1, 2 * h + 1);
 #pragma unroll
-                            for (int c = 0; c < NT; ++c)
-                                mma16816(part[i][c], a0, a1, a2, a3, h ? x[c].z : x[c].x, h ? x[c].w : x[c].y);
+                            for (int c = 0; c < NT; ++c) {
+                                const uint32_t b0 = h ? x[c].z : x[c].x, b1 = h ? x[c].w : x[c].y;
+                                if (first && h == 0) mma16816_first(part[i][c], a0, a1, a2, a3, b0, b1);
+                                else mma16816(part[i][c], a0, a1, a2, a3, b0, b1);
+                            }
                         }
                     }
                     if (((j + 1) * (kW4Block / G)) % 4 == 0) {   // word j ends a group
@@ -318,7 +313,7 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, uint32_
                         const bool have = (kb0 * (kW4Block / G) + gi) < ng;
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const uint32_t sa = base + S::S_OFF + (gi * kRows + tile_row(i) + pg) * 2;
+                            const uint8_t* sa = base + S::S_OFF + (gi * kRows + tile_row(i) + pg) * 2;
                             const float f0 = lds_bf16(sa), f1 = lds_bf16(sa + 16);
                             if (have) {   // past the last group all weights are 0
 #pragma unroll
@@ -443,7 +438,7 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
             pdl_wait();
             pdl_launch();
         }
-        consume<EPI, G, NT>(p, sh, smem_u32(smem), s_out, stages, pl, w);
+        consume<EPI, G, NT>(p, sh, smem, s_out, stages, pl, w);
     }
 }
 
