@@ -48,7 +48,6 @@ struct W4FfnArgs {
     int32_t* count;        // [2][kW4Counters], zero between calls
     WsHeader* hdr;
 };
-constexpr int kW4GemvSmem = 72 * 1024;
 int w4_gemv_ctas(int sms);
 int64_t w4_part_bytes();
 cudaError_t launch_w4_quantize(int64_t mats, int64_t rows, int64_t k, int group, int dtype, const void* w, uint8_t* q,

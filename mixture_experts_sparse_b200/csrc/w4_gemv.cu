@@ -42,7 +42,9 @@ constexpr int kWBytes = kRows * kStageBlocks * kW4BlockBytes;   // 16 KB
 constexpr int kXBytes = 8 * kStageK * 2;         // per 8 columns
 constexpr int kOutPitch = kRows + 4;             // conflict-free accumulator writes
 constexpr int kMaxStages = 8;
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = kWarps == 4 ? 3 : 2;
+constexpr int kSmem = kWarps == 4 ? 72 * 1024 : 110 * 1024;   // of a CTA
+constexpr int kBoxRows = 64, kBoxBytes = kBoxRows * 128;       // one TMA box of weights
 constexpr int kMinSteps = 2;                     // stages per CTA at least
 constexpr int kPartFloats = 16 * kRows;          // one fp32 part of a tile
 
@@ -109,24 +111,24 @@ struct Shared {
 // `steps` pipeline stages.
 struct Plan {
     int tiles, steps, chunk;   // feature tiles; stages per unit; rows per chunk
-    int64_t units, total;      // total = units * steps
+    int units, total;          // total = units * steps
     int ctas;
-    __device__ int64_t begin(int c) const { return total * c / ctas; }
-    __device__ int cta_of(int64_t step) const { return (int)(((step + 1) * ctas - 1) / total); }
+    __device__ int begin(int c) const { return (int)((int64_t)total * c / ctas); }
+    __device__ int cta_of(int step) const { return (int)(((int64_t)(step + 1) * ctas - 1) / total); }
 };
 
 struct Unit {
     int e, m0, row0, n;
 };
 
-__device__ __forceinline__ Unit unit_of(const Shared& sh, const Plan& pl, int64_t u, int feats) {
+__device__ __forceinline__ Unit unit_of(const Shared& sh, const Plan& pl, int u, int feats) {
     int lo = 0, hi = sh.live;   // first[lo] <= u < first[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (sh.first[mid] <= u) lo = mid;
         else hi = mid;
     }
-    const int e = sh.exp[lo], local = (int)(u - sh.first[lo]);
+    const int e = sh.exp[lo], local = u - sh.first[lo];
     const int chunks = (sh.row[e + 1] - sh.row[e] + pl.chunk - 1) / pl.chunk;
     Unit t;   // the chunks of a feature tile follow one another: its weights are in L2
     t.e = e;
@@ -138,12 +140,11 @@ __device__ __forceinline__ Unit unit_of(const Shared& sh, const Plan& pl, int64_
 
 // A position in the list.
 struct Cursor {
-    int64_t u;
-    int ks;
+    int u, ks;
     Unit t;
-    __device__ void start(const Shared& sh, const Plan& pl, int64_t step, int feats) {
+    __device__ void start(const Shared& sh, const Plan& pl, int step, int feats) {
         u = step / pl.steps;
-        ks = (int)(step - u * pl.steps);
+        ks = step - u * pl.steps;
         t = unit_of(sh, pl, u, feats);
     }
     __device__ void next(const Shared& sh, const Plan& pl, int feats) {
@@ -184,19 +185,20 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
             cp16(xd + v * 64, p.x + at, in);
             if (S::HILO) cp16(xd + (4 * NT + v) * 64, p.x_lo + at, in);
         }
-        // scales: 16 lanes a group, 8 tile rows a lane
-        const int r = (lane & 15) * 8;        // tile row
+        // scales: 8 tile rows a lane
+        constexpr int LANES = kRows / 8;
+        const int r = lane % LANES * 8;       // tile row
         const uint16_t* sc = S::MATS == 2 && r >= S::FEATS ? p.sb : p.sa;
         const int f = c.t.m0 + (S::MATS == 2 ? r % S::FEATS : r);
 #pragma unroll
-        for (int i = 0; i < S::SGROUPS; i += 2) {
-            const int gi = i + (lane >> 4), g = k0 / G + gi;
+        for (int i = 0; i < S::SGROUPS; i += 32 / LANES) {
+            const int gi = i + lane / LANES, g = k0 / G + gi;
             const bool have = g < ng && f < p.m_dim;
             cp16(base + S::S_OFF + gi * kRows * 2 + r * 2, have ? sc + ((int64_t)c.t.e * ng + g) * p.m_dim + f : p.sa, have);
         }
         cp_arrive(smem_u32(&sh.full[st]));
     };
-    const int64_t begin = pl.begin(blockIdx.x), end = pl.begin(blockIdx.x + 1);
+    const int begin = pl.begin(blockIdx.x), end = pl.begin(blockIdx.x + 1);
     Cursor cur;
     cur.start(sh, pl, begin, S::FEATS);
     Cursor late = cur;               // stage 2: the first stages' rows, asked for after the wait
@@ -211,7 +213,7 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
         }
     };
     uint32_t phase = 0, used = 0;
-    for (int64_t step = begin; step < end; ++step) {
+    for (int step = begin; step < end; ++step) {
         if (!waited && pending == stages) catch_up();   // the ring is full of weights
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.empty[stage]), phase ^ 1u, w));
         if (!ok) break;
@@ -219,10 +221,13 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
             const int kb = cur.ks * kStageBlocks * kW4BlockBytes;
             const uint32_t fb = smem_u32(&sh.full[stage]), base = ring + stage * S::STAGE;
             const int row = cur.t.e * p.m_dim + cur.t.m0;
-            const bool second = S::MATS == 2 || cur.t.m0 + 64 < p.m_dim;   // the upper 64 rows hold something
-            mbar_expect_tx(fb, second ? kWBytes : kWBytes / 2);
-            tma_load_2d(base, ma, fb, kb, row);
-            if (second) tma_load_2d(base + kWBytes / 2, S::MATS == 2 ? mb : ma, fb, kb, S::MATS == 2 ? row : row + 64);
+            constexpr int BOXES = kRows / kBoxRows, PER = BOXES / S::MATS;   // boxes of a matrix
+            const int live = min(PER, (p.m_dim - cur.t.m0 + kBoxRows - 1) / kBoxRows);   // those that hold something
+            mbar_expect_tx(fb, live * S::MATS * kBoxBytes);
+#pragma unroll
+            for (int b = 0; b < BOXES; ++b)
+                if (b % PER < live)
+                    tma_load_2d(base + b * kBoxBytes, b < PER ? ma : mb, fb, kb, row + b % PER * kBoxRows);
         }
         __syncwarp();
         used |= 1u << stage;
@@ -257,11 +262,11 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
     int stage = 0;
     uint32_t phase = 0;
     bool dead = false;
-    int64_t step = pl.begin(blockIdx.x);
-    const int64_t end = pl.begin(blockIdx.x + 1);
+    int step = pl.begin(blockIdx.x);
+    const int end = pl.begin(blockIdx.x + 1);
     while (step < end) {
-        const int64_t u = step / pl.steps, u0 = u * pl.steps, u1 = u0 + pl.steps;
-        const int64_t stop = min(end, u1);
+        const int u = step / pl.steps, u0 = u * pl.steps, u1 = u0 + pl.steps;
+        const int stop = min(end, u1);
         const Unit un = unit_of(sh, pl, u, S::FEATS);
         float acc[2][NT][4];
 #pragma unroll
@@ -270,12 +275,12 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
             for (int c = 0; c < NT; ++c)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[i][c][r] = 0.f;
-        const int64_t from = step;
+        const int from = step;
         for (; step < stop; ++step) {
             // after an abort the warp only keeps the barriers going
             if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(smem_u32(&sh.full[stage]), phase, w));
             const uint8_t* base = ring + stage * S::STAGE;
-            const int kb0 = (int)(step - u0) * kStageBlocks;
+            const int kb0 = (step - u0) * kStageBlocks;
 #pragma unroll
             for (int b = 0; b < kStageBlocks; ++b) {
                 if (dead || kb0 + b >= nb) break;   // a block past K holds nothing
@@ -359,20 +364,26 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
             const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u1 - 1);
             float* dst = p.part + ((int64_t)blockIdx.x * 2 + (from > u0 ? 0 : 1)) * kPartFloats;
             for (int col = 0; col < un.n; ++col) __stcg(dst + col * kRows + tid, s_out[col * kOutPitch + tid]);
-            __threadfence();
             named_bar(1, kRows);
-            if (tid == 0) {
+            if (tid == 0) {   // the barrier orders the CTA's stores before this thread's fence
+                __threadfence();
                 const int before = atomicAdd(p.count + c0, 1);
                 sh.last = before == c1 - c0;
                 if (before == c1 - c0) p.count[c0] = 0;
+                __threadfence();
             }
             named_bar(1, kRows);
             if (!sh.last) continue;
-            __threadfence();
-            for (int col = 0; col < un.n; ++col) {
-                float v = 0.f;
-                for (int c = c0; c <= c1; ++c)   // K order
-                    v += __ldcg(p.part + ((int64_t)c * 2 + (pl.begin(c) > u0 ? 0 : 1)) * kPartFloats + col * kRows + tid);
+            for (int col = 0; col < un.n; ++col) {   // in K order, eight loads at a time
+                const float* src = p.part + col * kRows + tid;
+                float v = __ldcg(src + ((int64_t)c0 * 2 + (pl.begin(c0) > u0 ? 0 : 1)) * kPartFloats);
+                for (int c = c0 + 1; c <= c1; c += 8) {   // the later parts start inside the tile: slot 0
+                    float q[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) q[i] = c + i <= c1 ? __ldcg(src + (int64_t)(c + i) * 2 * kPartFloats) : 0.f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v += q[i];
+                }
                 s_out[col * kOutPitch + tid] = v;
             }
             named_bar(1, kRows);
@@ -406,23 +417,42 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
     pl.chunk = S::CHUNK;
     pl.tiles = (p.m_dim + S::FEATS - 1) / S::FEATS;
     pl.steps = (p.k_dim + kStageK - 1) / kStageK;
-    if (tid == 0) {   // live experts and their first units
-        int c = 0, u = 0;
-        for (int e = 0; e < p.N; ++e) {
-            const int n = sh.row[e + 1] - sh.row[e];
-            if (n <= 0) continue;
-            sh.exp[c] = e;
-            sh.first[c++] = u;
-            u += (n + S::CHUNK - 1) / S::CHUNK * pl.tiles;
+    if (tid < 32) {   // live experts and their first units: four experts a lane, a scan over the lanes
+        int n[4], live = 0, units = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = 4 * tid + i;
+            n[i] = e < p.N ? max(0, sh.row[e + 1] - sh.row[e]) : 0;
+            live += n[i] > 0;
+            units += (n[i] + S::CHUNK - 1) / S::CHUNK * pl.tiles;
         }
-        sh.first[c] = u;
-        sh.live = c;
+        int l = live, u = units;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int lo = __shfl_up_sync(0xffffffffu, l, o), uo = __shfl_up_sync(0xffffffffu, u, o);
+            if (tid >= o) {
+                l += lo;
+                u += uo;
+            }
+        }
+        if (tid == 31) {
+            sh.live = l;
+            sh.first[l] = u;
+        }
+        l -= live;
+        u -= units;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n[i] > 0) {
+                sh.exp[l] = 4 * tid + i;
+                sh.first[l++] = u;
+                u += (n[i] + S::CHUNK - 1) / S::CHUNK * pl.tiles;
+            }
     }
     __syncthreads();
     pl.units = sh.first[sh.live];
     pl.total = pl.units * pl.steps;
-    const int64_t most = (pl.total + kMinSteps - 1) / kMinSteps;
-    pl.ctas = (int)(most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x);
+    pl.ctas = min((pl.total + kMinSteps - 1) / kMinSteps, (int)gridDim.x);
     if ((int)blockIdx.x >= pl.ctas) {
         pdl_wait();
         pdl_launch();
@@ -490,18 +520,18 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 
 // packed rows [rows][pitch] bytes: boxes of 64 rows x 128 bytes, 128-byte swizzle
 bool make_map_w4(CUtensorMap* map, const void* q, int64_t rows, int64_t pitch) {
-    return make_map_u8(map, q, rows, pitch, 64);
+    return make_map_u8(map, q, rows, pitch, kBoxRows);
 }
 
 template <int EPI, int G>
 cudaError_t run_gemv_g(const CUtensorMap& a, const CUtensorMap& b, GemvParams p, int sms, cudaStream_t s) {
     auto kern = w4_gemv_kernel<EPI, G>;
     cudaError_t err = once_per_device(reinterpret_cast<const void*>(kern), [](const void* k) {
-        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kW4GemvSmem);
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
     if (err != cudaSuccess) return err;
-    p.smem_bytes = kW4GemvSmem;
-    return launch_k(kern, dim3((unsigned)w4_gemv_ctas(sms)), dim3(kThreads), kW4GemvSmem, s, 1, a, b, p);
+    p.smem_bytes = kSmem;
+    return launch_k(kern, dim3((unsigned)w4_gemv_ctas(sms)), dim3(kThreads), kSmem, s, 1, a, b, p);
 }
 
 template <int EPI>
