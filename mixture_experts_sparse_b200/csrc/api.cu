@@ -711,16 +711,30 @@ int32_t moe_expert_ffn(const moe_config* cfg, const void* xe, const int32_t* off
 
 static bool w4_group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
 
-// the layer workspace, then what H's rounding to bf16 left (h_lo), then the sums
-// of tiles that CTAs share
-static size_t w4_lo_offset(const Layout& L) { return L.total; }
-static size_t w4_part_offset(const moe_config& c, const Layout& L) {
+// the layer workspace, then the rows of x and H as integers with their units, then
+// the sums of tiles that CTAs share
+struct W4Layout {
+    size_t xq, xu, hq, hu, part, total;
+};
+static W4Layout w4_layout(const moe_config& c, const Layout& L) {
+    W4Layout w{};
+    size_t off = L.total;
+    auto take = [&](size_t bytes) {
+        size_t o = off;
+        off += round_up(bytes, 256);
+        return o;
+    };
     const size_t R = (size_t)(L.rows > 0 ? L.rows : 1);
-    return L.total + round_up(2 * R * (size_t)c.d_ff, 256);
+    const size_t d = (size_t)w4_padded(c.d_model), f = (size_t)w4_padded(c.d_ff);
+    w.xq = take(2 * R * d);
+    w.xu = take(4 * R * (d / kW4ActBlock));
+    w.hq = take(2 * R * f);
+    w.hu = take(4 * R * (f / kW4ActBlock));
+    w.part = take((size_t)w4_part_bytes());
+    w.total = off;
+    return w;
 }
-static size_t w4_total(const moe_config& c, const Layout& L) {
-    return w4_part_offset(c, L) + (size_t)w4_part_bytes();
-}
+static size_t w4_total(const moe_config& c, const Layout& L) { return w4_layout(c, L).total; }
 
 size_t moe_w4_row_bytes(int64_t k) { return k < 0 ? 0 : (size_t)w4_row_bytes(k); }
 
@@ -791,10 +805,13 @@ static int32_t w4_ffn_impl(const moe_config* cfg, const W4Weights& w, const void
     a.b1 = static_cast<const __nv_bfloat16*>(w.b1);
     a.b3 = static_cast<const __nv_bfloat16*>(w.b3);
     a.b2 = static_cast<const __nv_bfloat16*>(w.b2);
-    a.h = at<__nv_bfloat16>(ws, L.h);
-    a.h_lo = at<__nv_bfloat16>(ws, w4_lo_offset(L));
+    const W4Layout W = w4_layout(*cfg, L);
+    a.xq = at<uint8_t>(ws, W.xq);
+    a.xu = at<float>(ws, W.xu);
+    a.hq = at<uint8_t>(ws, W.hq);
+    a.hu = at<float>(ws, W.hu);
     a.ye = static_cast<__nv_bfloat16*>(ye);
-    a.part = at<float>(ws, w4_part_offset(*cfg, L));
+    a.part = at<float>(ws, W.part);
     a.count = at<int32_t>(ws, L.w4_count);
     a.hdr = at<WsHeader>(ws, L.hdr);
     return cuda_status(launch_w4_ffn(a, s));

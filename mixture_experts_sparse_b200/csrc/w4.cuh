@@ -1,13 +1,13 @@
-// 4-bit weights with group scales: layout and decoding (internal header).
+// 4-bit weights with group scales: layout (internal header).
 //
 // A row of K weights is cut into blocks of 128, 64 bytes each (the last block is
 // padded with zero weights).  Word 4 t + j (t, j = 0..3) of a block holds its
 // weights k = 32 j + 8 t .. + 7, as q + 8 in 4 bits: k + 2 i in bits 4 i, k + 2 i + 1
 // in bits 16 + 4 i.  So (a) the 16 bytes that lane t of a quad loads give, word
-// by word, the A fragments of m16n8k16 for 32 consecutive k -- a group scale
-// never cuts a fragment, and the matching B fragment is 16 consecutive bytes of
-// the token's row; (b) one shift, one logic operation and one subtraction
-// decode an adjacent pair.
+// by word, the A fragments of m16n8k32 for 32 consecutive k, and a group scale
+// never cuts a fragment; (b) the even and the odd nibbles of a word, as the upper
+// halves of four bytes each, are 16 q in two's complement after one exclusive or;
+// (c) one shift and one logic operation give an adjacent pair as bf16.
 // Scales are bf16, [matrix][group][row]: the scales of a tile's rows are adjacent.
 #pragma once
 
@@ -26,23 +26,26 @@ struct W4Mat {            // one weight matrix per expert: [N][rows][K]
     const uint16_t* s;    // [N][groups][rows] bf16
 };
 
-// Weights 2 p and 2 p + 1 of the word's eight as a bf16 pair: 128 + (q + 8) is
-// exact in bf16 (0x4300 is 128, whose last place is 1), and so is the difference.
-__device__ __forceinline__ uint32_t w4_pair(uint32_t w, int p) {
-    uint32_t u;   // (w >> 4 p & mask) | magic in one operation (two immediates would make it two)
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
-    const uint32_t c = 0x43084308u;   // 136, 136
-    __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&c));
-    return *reinterpret_cast<uint32_t*>(&r);
-}
+// Rows of activations for the few-row kernels: blocks of 64 values as 16-bit
+// integers X = rint(v / unit) with their own unit, max |v| / 32512, held as two
+// signed bytes, X = 256 hi + lo.  A block is 128 bytes, hi then lo; its 64 bytes
+// are the B fragments of two k-steps: for t, j = 0..3, 0..1 the eight values k =
+// 32 j + 8 t .. + 7 at 16 t + 8 j, in the order 0 4 1 5 2 6 3 7 of the words'
+// nibbles.  Rows are padded to 256 values; units are fp32 [R][padded / 64], divided
+// by 16 (the weights' bytes are 16 q).  A block that holds a NaN or infinity has
+// unit NaN; magnitudes below 2^-100 count as 0.
+constexpr int kW4ActBlock = 64;
+inline __host__ __device__ int64_t w4_padded(int64_t k) { return (k + 255) / 256 * 256; }
 
 struct W4FfnArgs {
     int act; int N; int d; int d_ff; int group; int64_t R_cap;
     const __nv_bfloat16* xe; const int32_t* offsets;
     W4Mat w1, w3, w2;
     const __nv_bfloat16* b1; const __nv_bfloat16* b3; const __nv_bfloat16* b2;
-    __nv_bfloat16* h;      // [R_cap, d_ff]
-    __nv_bfloat16* h_lo;   // [R_cap, d_ff]: what h's rounding left (few rows)
+    uint8_t* xq;           // [R_cap][w4_padded(d)] x 2 bytes: xe as integers
+    float* xu;             // [R_cap][w4_padded(d) / 64]: their units
+    uint8_t* hq;           // [R_cap][w4_padded(d_ff)] x 2 bytes: H
+    float* hu;
     __nv_bfloat16* ye;     // [R_cap, d]
     float* part;           // w4_part_bytes(): sums of tiles that CTAs share
     int32_t* count;        // [2][kW4Counters], zero between calls

@@ -4,22 +4,28 @@
 //   stage 1: H = relu(x W1^T + b1), or silu(x W1^T + b1) * (x W3^T + b3)
 //   stage 2: y = H W2^T + b2              W[o][k] = q[o][k] s[o][k / G]
 //
+// Decoding is what a matrix-vector kernel on 4-bit weights has to get out of the
+// way: at the rate of HBM an SM receives about 46 weights a cycle and has 128
+// lanes for everything.  Decoded to bf16 a weight costs 1.4 operations (a
+// measured kernel stayed at 3.5 TB/s, bound by the integer pipe); as bytes of
+// the integer mma.sync m16n8k32 it costs 3/8: one word gives two fragment
+// registers by a shift and two logic operations.  So the rows of x (and H)
+// are turned into integers, 16 bits per value in blocks of 64 with a unit each
+// (w4.cuh), two columns of bytes per token.  Integer sums are exact; per block
+// of 64 the two bytes' sums join in fp32 and the unit and the group's scale
+// multiply them.  The rounding of x is below 2^-16 of its block's largest value,
+// against 2^-9 of y's own rounding to bf16.
+// tcgen05 with at most 16 tokens would decode the same words, into shared memory
+// or TMEM, for a product that takes a few per cent of the time here.
+//
 // A CTA has four consumer warps and a producer warp.  Its tile is 128 weight rows
-// (64 features of W1 and the same of W3 for SwiGLU) by up to 16 columns, a
+// (64 features of W1 and the same of W3 for SwiGLU) by up to 16 tokens, a
 // pipeline stage 256 of K: the producer brings the packed rows with TMA
 // (128-byte swizzle) and the tokens' rows and the group scales with cp.async
-// into an mbarrier ring.  A consumer warp owns 32 weight rows as two m16n8k16
-// tiles; its 16-byte shared loads are, word by word, the A fragments (w4.cuh),
-// decoded to bf16 exactly as integers, so the products of a group are exact in
-// the fp32 accumulator and the group's scale multiplies their sum in fp32.
-// Lane g of an mma row group reads tile row perm(g): rows 0 4 1 5 2 6 3 7, whose
-// swizzled 16-byte chunks fall into different banks.
-// mma.sync and not tcgen05: with at most 16 tokens the tensor work is a few
-// per cent of either pipe, decoding and HBM bound the loop, and register
-// fragments save the way through shared memory or TMEM that a tcgen05 operand
-// takes.
-// H keeps two bf16 parts, its rounding and the remainder (16 bits in all): stage
-// 2 takes them as two columns per token, so the output has one rounding.
+// into an mbarrier ring.  A consumer warp owns 32 weight rows as two m16 tiles;
+// its 16-byte shared loads are, word by word, the A fragments.  Lane g of an mma
+// row group reads tile row perm(g): rows 0 4 1 5 2 6 3 7, whose swizzled 16-byte
+// chunks fall into different banks.
 //
 // The pipeline stages of all tiles form one list, cut into equal ranges, one per
 // CTA, so that every SM streams the same number of bytes whatever the sizes.  A
@@ -39,8 +45,8 @@ constexpr int kRows = 32 * kWarps;               // weight rows of a tile
 constexpr int kStageBlocks = 2;                  // 128-weight blocks of K per stage
 constexpr int kStageK = kStageBlocks * kW4Block;
 constexpr int kWBytes = kRows * kStageBlocks * kW4BlockBytes;   // 16 KB
-constexpr int kXBytes = 8 * kStageK * 2;         // per 8 columns
-constexpr int kOutPitch = kRows + 4;             // conflict-free accumulator writes
+constexpr int kXBytes = 8 * kStageK;             // per 8 columns of bytes (4 tokens)
+constexpr int kOutPitch = kRows + 8;             // conflict-free accumulator writes
 constexpr int kMaxStages = 8;
 constexpr int kCtasPerSm = kWarps == 4 ? 3 : 2;
 constexpr int kSmem = kWarps == 4 ? 72 * 1024 : 110 * 1024;   // of a CTA
@@ -56,8 +62,9 @@ struct GemvParams {
     int k_dim;
     const uint16_t* sa; const uint16_t* sb;              // scales (sb: W3)
     const __nv_bfloat16* bias_a; const __nv_bfloat16* bias_b;
-    const __nv_bfloat16* x; const __nv_bfloat16* x_lo;   // [R, k_dim]
-    __nv_bfloat16* out; __nv_bfloat16* out_lo;           // [R, m_dim]
+    const uint8_t* x; const float* xu;                   // rows as integers, their units
+    __nv_bfloat16* out;                                  // stage 2: [R, m_dim]
+    uint8_t* hq; float* hu;                              // stage 1: H as integers
     float* part;                  // [CTAs][2][kPartFloats]
     int32_t* count;               // [CTAs] arrivals per shared tile, zero between calls
     int32_t* clear;               // [clear_n] the other stage's counters
@@ -67,21 +74,52 @@ struct GemvParams {
     long long limit_ns;
 };
 
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-
-// the first product of a group: c = a b
-__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                               uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+// The first product of a block: c = kMagic + a b.  As bits of a float that is
+// 1.5 2^23 + the sum, exact while the sum stays below 2^22 (64 products of at most
+// 128 x 128 are 2^20): the conversion to fp32 is one subtraction.
+constexpr int kMagic = 0x4B400000;
+__device__ __forceinline__ void mma_s8_first(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%10, %10, %10, %10};"
-        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+        : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(kMagic));
+}
+__device__ __forceinline__ float magic_sum(int c) { return __int_as_float(c) - 12582912.f; }
+
+// (w ^ 0x88888888) & 0xF0F0F0F0: the odd nibbles as bytes 16 q
+__device__ __forceinline__ uint32_t odd_nibbles(uint32_t w) {
+    uint32_t u;
+    asm("lop3.b32 %0, %1, %2, %3, 0x28;" : "=r"(u) : "r"(w), "r"(0x88888888u), "r"(0xF0F0F0F0u));
+    return u;
+}
+
+// Eight values of a row as integers: bytes hi and lo of rint(v inv), in fragment order.
+__device__ __forceinline__ void to_bytes(const float (&v)[8], float inv, uint2& hi, uint2& lo) {
+    uint32_t h[2] = {0, 0}, l[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int k = i / 4 * 2 + (i >> 1 & 1) + 4 * (i & 1);   // 0 4 1 5 2 6 3 7
+        const int X = __float2int_rn(v[k] * inv), b = (X + 128 & 255) - 128;
+        h[i / 4] |= (uint32_t)((X - b) >> 8 & 255) << (8 * (i & 3));
+        l[i / 4] |= (uint32_t)(b & 255) << (8 * (i & 3));
+    }
+    hi = make_uint2(h[0], h[1]);
+    lo = make_uint2(l[0], l[1]);
+}
+// the unit (over 16) and its reciprocal for a block's largest magnitude, given as bits
+__device__ __forceinline__ void block_unit(uint32_t max_bits, float& unit16, float& inv) {
+    const float m = __uint_as_float(max_bits);
+    const bool finite = max_bits < 0x7F800000u, some = finite && m >= 7.8886e-31f;   // 2^-100
+    inv = some ? 32512.f / m : 0.f;
+    unit16 = some ? m * (1.f / (16.f * 32512.f)) : (finite ? 0.f : __uint_as_float(0x7FC00000u));
 }
 
 // 16 bytes global -> shared; ok = false fills zeros
@@ -158,11 +196,11 @@ template <int EPI, int G, int NT>
 struct Shape {
     static constexpr int MATS = EPI == W4_SWIGLU ? 2 : 1;
     static constexpr int FEATS = kRows / MATS;                   // output features of a tile
-    static constexpr bool HILO = EPI == W4_OUT;
-    static constexpr int CHUNK = HILO ? 4 * NT : 8 * NT;         // tokens of a tile (two columns each with HILO)
+    static constexpr int CHUNK = 4 * NT;                         // tokens of a tile, two columns each
     static constexpr int SGROUPS = kStageK / G;                  // groups per stage
     static constexpr int X_OFF = kWBytes;
-    static constexpr int S_OFF = X_OFF + NT * kXBytes;
+    static constexpr int U_OFF = X_OFF + NT * kXBytes;           // units: 4 floats a token
+    static constexpr int S_OFF = U_OFF + CHUNK * 16;
     static constexpr int STAGE = (S_OFF + SGROUPS * kRows * 2 + 1023) / 1024 * 1024;
     static constexpr int OUT_BYTES = CHUNK * kOutPitch * 4;
 };
@@ -173,18 +211,17 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
     using S = Shape<EPI, G, NT>;
     const int lane = threadIdx.x & 31;
     const int ng = (p.k_dim + G - 1) / G;
-    // the rows of x and the scales of the stage at c
+    const int64_t padded = w4_padded(p.k_dim);
+    // the rows of x, their units and the scales of the stage at c
     auto rows_of = [&](const Cursor& c, int st) {
         const int k0 = c.ks * kStageK;
         const uint32_t base = ring + st * S::STAGE;
-        const int k = k0 + 8 * lane;          // this lane's 8 of the row's 256
-        const uint32_t xd = base + S::X_OFF + (lane >> 2) * (8 * NT * 64) + (lane & 3) * 16;
-        const bool in = k < p.k_dim;
-        int64_t at = (int64_t)c.t.row0 * p.k_dim + (in ? k : 0);
-        for (int v = 0; v < c.t.n; ++v, at += p.k_dim) {
-            cp16(xd + v * 64, p.x + at, in);
-            if (S::HILO) cp16(xd + (4 * NT + v) * 64, p.x_lo + at, in);
-        }
+        // a token's 512 bytes: [block of 64][hi, lo][t][16], into [block][column][t][16]
+        const uint32_t xd = base + S::X_OFF + (lane >> 3) * (8 * NT * 64) + (lane >> 2 & 1) * 64 + (lane & 3) * 16;
+        const uint8_t* xs = p.x + ((int64_t)c.t.row0 * padded + k0) * 2 + lane * 16;
+        for (int v = 0; v < c.t.n; ++v) cp16(xd + v * 128, xs + v * padded * 2, true);
+        if (lane < c.t.n)
+            cp16(base + S::U_OFF + lane * 16, p.xu + ((int64_t)(c.t.row0 + lane) * padded + k0) / kW4ActBlock, true);
         // scales: 8 tile rows a lane
         constexpr int LANES = kRows / 8;
         const int r = lane % LANES * 8;       // tile row
@@ -201,9 +238,9 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
     const int begin = pl.begin(blockIdx.x), end = pl.begin(blockIdx.x + 1);
     Cursor cur;
     cur.start(sh, pl, begin, S::FEATS);
-    Cursor late = cur;               // stage 2: the first stages' rows, asked for after the wait
+    Cursor late = cur;               // the first stages' rows, asked for after the wait
     int pending = 0, stage = 0;
-    bool waited = EPI != W4_OUT, ok = true;
+    bool waited = false, ok = true;
     auto catch_up = [&]() {
         pdl_wait();
         waited = true;
@@ -268,19 +305,20 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
         const int u = step / pl.steps, u0 = u * pl.steps, u1 = u0 + pl.steps;
         const int stop = min(end, u1);
         const Unit un = unit_of(sh, pl, u, S::FEATS);
-        float acc[2][NT][4];
+        float acc[2][NT][2];   // [m16 tile][column block][row pg, pg + 8] of token 4 c + t
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][c][r] = 0.f;
+            for (int c = 0; c < NT; ++c) acc[i][c][0] = acc[i][c][1] = 0.f;
         const int from = step;
         for (; step < stop; ++step) {
             // after an abort the warp only keeps the barriers going
             if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(smem_u32(&sh.full[stage]), phase, w));
             const uint8_t* base = ring + stage * S::STAGE;
             const int kb0 = (step - u0) * kStageBlocks;
+            float4 unit[NT];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) unit[c] = *reinterpret_cast<const float4*>(base + S::U_OFF + (4 * c + t) * 16);
 #pragma unroll
             for (int b = 0; b < kStageBlocks; ++b) {
                 if (dead || kb0 + b >= nb) break;   // a block past K holds nothing
@@ -290,44 +328,46 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
                         wd[i][h] = lds16(base + (tile_row(i) + 8 * h + pg) * 128 + (((4 * b + t) ^ pg) << 4));
-                float part[2][NT][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool first = (j * (kW4Block / G)) % 4 == 0;   // word j starts a group
-                    uint4 x[NT];
+                for (int q = 0; q < 2; ++q) {   // blocks of 64 values
+                    if ((kb0 + b) * kW4Block + q * kW4ActBlock >= p.k_dim) break;
+                    uint4 x[NT];   // a column that no token fills holds anything: it is not read back
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)   // a column that no token fills holds anything: it is not read back
-                        x[c] = lds16(base + S::X_OFF + ((4 * b + j) * 8 * NT + 8 * c + g) * 64 + t * 16);
+                    for (int c = 0; c < NT; ++c)
+                        x[c] = lds16(base + S::X_OFF + ((2 * b + q) * 8 * NT + 8 * c + g) * 64 + t * 16);
+                    int part[2][NT][4];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t w0 = word_of(wd[i][0], j), w1 = word_of(wd[i][1], j);
+                    for (int jj = 0; jj < 2; ++jj) {
+                        const int j = 2 * q + jj;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint32_t a0 = w4_pair(w0, 2 * h), a1 = w4_pair(w1, 2 * h);
-                            const uint32_t a2 = w4_pair(w0, 2 * h + 1), a3 = w4_pair(w1, 2 * h + 1);
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t w0 = word_of(wd[i][0], j), w1 = word_of(wd[i][1], j);
+                            const uint32_t a0 = odd_nibbles(w0 << 4), a1 = odd_nibbles(w1 << 4);
+                            const uint32_t a2 = odd_nibbles(w0), a3 = odd_nibbles(w1);
 #pragma unroll
                             for (int c = 0; c < NT; ++c) {
-                                const uint32_t b0 = h ? x[c].z : x[c].x, b1 = h ? x[c].w : x[c].y;
-                                if (first && h == 0) mma16816_first(part[i][c], a0, a1, a2, a3, b0, b1);
-                                else mma16816(part[i][c], a0, a1, a2, a3, b0, b1);
+                                const uint32_t b0 = jj ? x[c].z : x[c].x, b1 = jj ? x[c].w : x[c].y;
+                                if (jj == 0 || G == 32) mma_s8_first(part[i][c], a0, a1, a2, a3, b0, b1);
+                                else mma_s8(part[i][c], a0, a1, a2, a3, b0, b1);
                             }
                         }
-                    }
-                    if (((j + 1) * (kW4Block / G)) % 4 == 0) {   // word j ends a group
+                        if (jj == 0 && G > 32) continue;
+                        // the block's (or group's) sums join: 256 hi + lo, times the unit and the scale
                         const int gi = b * (kW4Block / G) + j * (kW4Block / G) / 4;   // group of the stage
-                        const bool have = (kb0 * (kW4Block / G) + gi) < ng;
+                        if (kb0 * (kW4Block / G) + gi >= ng) continue;                // a last block shorter than 64
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint8_t* sa = base + S::S_OFF + (gi * kRows + tile_row(i) + pg) * 2;
                             const float f0 = lds_bf16(sa), f1 = lds_bf16(sa + 16);
-                            if (have) {   // past the last group all weights are 0
 #pragma unroll
-                                for (int c = 0; c < NT; ++c) {
-                                    acc[i][c][0] = fmaf(part[i][c][0], f0, acc[i][c][0]);
-                                    acc[i][c][1] = fmaf(part[i][c][1], f0, acc[i][c][1]);
-                                    acc[i][c][2] = fmaf(part[i][c][2], f1, acc[i][c][2]);
-                                    acc[i][c][3] = fmaf(part[i][c][3], f1, acc[i][c][3]);
-                                }
+                            for (int c = 0; c < NT; ++c) {
+                                const int qi = 2 * b + q;
+                                const float un64 = qi == 0 ? unit[c].x : qi == 1 ? unit[c].y : qi == 2 ? unit[c].z : unit[c].w;
+                                const int* pt = part[i][c];
+                                const float v0 = fmaf(magic_sum(pt[0]), 256.f, magic_sum(pt[1])) * un64;
+                                const float v1 = fmaf(magic_sum(pt[2]), 256.f, magic_sum(pt[3])) * un64;
+                                acc[i][c][0] = fmaf(v0, f0, acc[i][c][0]);
+                                acc[i][c][1] = fmaf(v1, f1, acc[i][c][1]);
                             }
                         }
                     }
@@ -343,22 +383,11 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
         // accumulators -> s_out[token][tile row]
         named_bar(1, kRows);   // the previous tile's values have been read
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (S::HILO) {   // a token's two columns: column v and v + 4 NT
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int c = 0; c < (NT + 1) / 2; ++c)
+            for (int c = 0; c < NT; ++c)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][c][r] += NT == 1 ? __shfl_down_sync(0xffffffffu, acc[i][c][r], 2) : acc[i][c + NT / 2][r];
-            }
-#pragma unroll
-            for (int c = 0; c < (S::HILO ? (NT + 1) / 2 : NT); ++c)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int col = 8 * c + 2 * t + (r & 1);
-                    if (col < S::CHUNK) s_out[col * kOutPitch + tile_row(i) + pg + 8 * (r >> 1)] = acc[i][c][r];
-                }
-        }
+                for (int r = 0; r < 2; ++r) s_out[(4 * c + t) * kOutPitch + tile_row(i) + pg + 8 * r] = acc[i][c][r];
         named_bar(1, kRows);
         if (from > u0 || stop < u1) {   // other CTAs hold the rest of the tile's K
             const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u1 - 1);
@@ -388,22 +417,94 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
             }
             named_bar(1, kRows);
         }
-        // bias, activation, output: a thread per feature, the columns dealt to the tile's MATS halves
+        // bias, activation: a thread per feature, the tokens dealt to the tile's MATS halves
         const int f = tid % S::FEATS, feat = un.m0 + f;
-        if (feat < p.m_dim) {
-            const int64_t bi = (int64_t)un.e * p.m_dim + feat;
-            const float ba = p.bias_a ? __bfloat162float(p.bias_a[bi]) : 0.f;
-            const float bb = S::MATS == 2 && p.bias_b ? __bfloat162float(p.bias_b[bi]) : 0.f;
-            for (int col = tid / S::FEATS; col < un.n; col += S::MATS) {
-                float o = s_out[col * kOutPitch + f] + ba;
-                if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
-                if (EPI == W4_SWIGLU)
-                    o = o / (1.f + fast_exp2(-o * kLog2e)) * (s_out[col * kOutPitch + S::FEATS + f] + bb);
-                const __nv_bfloat16 hi = __float2bfloat16_rn(o);
-                const int64_t at = (int64_t)(un.row0 + col) * p.m_dim + feat;
-                p.out[at] = hi;
-                if (EPI != W4_OUT) p.out_lo[at] = __float2bfloat16_rn(o - __bfloat162float(hi));
+        const bool in = feat < p.m_dim;
+        const int64_t bi = (int64_t)un.e * p.m_dim + feat;
+        const float ba = in && p.bias_a ? __bfloat162float(p.bias_a[bi]) : 0.f;
+        const float bb = S::MATS == 2 && in && p.bias_b ? __bfloat162float(p.bias_b[bi]) : 0.f;
+        for (int col = tid / S::FEATS; col < un.n; col += S::MATS) {
+            float o = s_out[col * kOutPitch + f] + ba;
+            if (EPI == W4_OUT) {
+                if (in) p.out[(int64_t)(un.row0 + col) * p.m_dim + feat] = __float2bfloat16_rn(o);
+                continue;
             }
+            if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
+            if (EPI == W4_SWIGLU)
+                o = o / (1.f + fast_exp2(-o * kLog2e)) * (s_out[col * kOutPitch + S::FEATS + f] + bb);
+            s_out[col * kOutPitch + f] = in ? o : 0.f;
+        }
+        if (EPI == W4_OUT) continue;
+        // H as integers: eight lanes per token and block of 64 features
+        named_bar(1, kRows);
+        constexpr int BLOCKS = S::FEATS / kW4ActBlock;
+        const int64_t padded = w4_padded(p.m_dim);
+        for (int k0 = 0; k0 < un.n * BLOCKS; k0 += kRows / 8) {
+            const int k = k0 + tid / 8, l = tid % 8;
+            const int col = k / BLOCKS, blk = k % BLOCKS;
+            const bool ok = k < un.n * BLOCKS && un.m0 + blk * kW4ActBlock < p.m_dim;
+            float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            if (ok) {
+                const float4* src = reinterpret_cast<const float4*>(s_out + col * kOutPitch + blk * kW4ActBlock + 8 * l);
+                const float4 a = src[0], b = src[1];
+                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            }
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float unit16, inv;
+            block_unit(m, unit16, inv);
+            uint2 hi, lo;
+            to_bytes(v, inv, hi, lo);
+            if (ok) {
+                const int64_t at = (int64_t)(un.row0 + col) * padded + un.m0 + blk * kW4ActBlock;   // in values
+                uint8_t* dst = p.hq + at * 2 + (l & 3) * 16 + (l >> 2) * 8;
+                *reinterpret_cast<uint2*>(dst) = hi;
+                *reinterpret_cast<uint2*>(dst + 64) = lo;
+                if (l == 0) p.hu[at / kW4ActBlock] = unit16;
+            }
+        }
+    }
+}
+
+// Rows of x as integers: eight lanes per block of 64 values.
+constexpr int kRowThreads = 256;
+__global__ void __launch_bounds__(kRowThreads)
+w4_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ offsets, int N, int64_t R_cap, int k_dim,
+               uint8_t* __restrict__ xq, float* __restrict__ xu) {
+    pdl_wait();
+    pdl_launch();
+    const int64_t last = offsets[N], rows = last < 0 ? 0 : (last > R_cap ? R_cap : last);
+    const int64_t padded = w4_padded(k_dim);
+    const int blocks = (k_dim + kW4ActBlock - 1) / kW4ActBlock, l = threadIdx.x & 7;
+    for (int64_t q0 = (int64_t)blockIdx.x * (kRowThreads / 8); q0 < rows * blocks; q0 += (int64_t)gridDim.x * (kRowThreads / 8)) {
+        const int64_t q = q0 + threadIdx.x / 8, row = q / blocks;
+        const int k = (int)(q - row * blocks) * kW4ActBlock + 8 * l;
+        const bool ok = q < rows * blocks;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (ok && k < k_dim) {
+            const uint4 a = *reinterpret_cast<const uint4*>(x + row * k_dim + k);
+            v[0] = bf16lo(a.x); v[1] = bf16hi(a.x); v[2] = bf16lo(a.y); v[3] = bf16hi(a.y);
+            v[4] = bf16lo(a.z); v[5] = bf16hi(a.z); v[6] = bf16lo(a.w); v[7] = bf16hi(a.w);
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float unit16, inv;
+        block_unit(m, unit16, inv);
+        uint2 hi, lo;
+        to_bytes(v, inv, hi, lo);
+        if (ok) {
+            const int64_t at = row * padded + k - 8 * l;
+            uint8_t* dst = xq + at * 2 + (l & 3) * 16 + (l >> 2) * 8;
+            *reinterpret_cast<uint2*>(dst) = hi;
+            *reinterpret_cast<uint2*>(dst + 64) = lo;
+            if (l == 0) xu[at / kW4ActBlock] = unit16;
         }
     }
 }
@@ -464,10 +565,8 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
     if (tid >= 32 * kWarps) {
         produce<EPI, G, NT>(p, ma, mb, sh, smem_u32(smem), stages, pl, w);
     } else {
-        if (EPI == W4_OUT) {
-            pdl_wait();
-            pdl_launch();
-        }
+        pdl_wait();
+        pdl_launch();
         consume<EPI, G, NT>(p, sh, smem, s_out, stages, pl, w);
     }
 }
@@ -491,12 +590,9 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         prefetch_tmap(&map_a);
         prefetch_tmap(&map_b);
     }
-    // Stage 2 may start while stage 1 drains: the offsets and the weights are
-    // inputs of both, so stage 2 reads them before it waits for stage 1's rows.
-    if (EPI != W4_OUT) {
-        pdl_wait();
-        pdl_launch();
-    }
+    // A stage may start while its predecessor (the rows' conversion, stage 1) drains:
+    // the offsets and the weights are inputs of the whole call, complete before
+    // the conversion began, so they are read before the wait for the rows.
     for (int i = tid; i <= p.N; i += kThreads) {
         const int64_t v = p.offsets[i];
         sh.row[i] = (int)(v < 0 ? 0 : (v > p.R_cap ? p.R_cap : v));
@@ -506,13 +602,14 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     __syncthreads();
     const int most = s_most;
     if (most > 0) {
-        if (most <= (EPI == W4_OUT ? 4 : 8)) run_tiles<EPI, G, 1>(p, &map_a, &map_b, sh, smem);
-        else run_tiles<EPI, G, 2>(p, &map_a, &map_b, sh, smem);
+        if (most <= 4) run_tiles<EPI, G, 1>(p, &map_a, &map_b, sh, smem);
+        else if (most <= 8) run_tiles<EPI, G, 2>(p, &map_a, &map_b, sh, smem);
+        else run_tiles<EPI, G, 4>(p, &map_a, &map_b, sh, smem);
     } else {
         pdl_wait();
         pdl_launch();
     }
-    // The other stage's counters: stage 1 clears stage 2's, which starts after
+    // The other stage's counters: stage 1 clears stage 2's, whose parts come after
     // it, and stage 2 (past its wait) those of the next call's stage 1.
     if (blockIdx.x == 0)
         for (int i = tid; i < p.clear_n; i += kThreads) p.clear[i] = 0;
@@ -571,11 +668,16 @@ cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     p.sb = a.w3.s;
     p.bias_a = a.b1;
     p.bias_b = a.b3;
-    p.x = a.xe;
-    p.out = a.h;
-    p.out_lo = a.h_lo;
+    p.x = a.xq;
+    p.xu = a.xu;
+    p.hq = a.hq;
+    p.hu = a.hu;
     p.count = a.count;
     p.clear = a.count + kW4Counters;
+    const int64_t row_blocks = (a.R_cap * ((a.d + kW4ActBlock - 1) / kW4ActBlock) + kRowThreads / 8 - 1) / (kRowThreads / 8);
+    err = launch_k(w4_rows_kernel, dim3((unsigned)(row_blocks < 8 * sms ? row_blocks : 8 * sms)), dim3(kRowThreads), 0, s, 1,
+                   a.xe, a.offsets, a.N, a.R_cap, a.d, a.xq, a.xu);
+    if (err != cudaSuccess) return err;
     err = a.act == MOE_SWIGLU ? run_gemv<W4_SWIGLU>(m1, m3, p, a.group, sms, s)
                               : run_gemv<W4_RELU>(m1, m3, p, a.group, sms, s);
     if (err != cudaSuccess) return err;
@@ -584,10 +686,9 @@ cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     p.sa = a.w2.s;
     p.bias_a = a.b2;
     p.bias_b = nullptr;
-    p.x = a.h;
-    p.x_lo = a.h_lo;
+    p.x = a.hq;
+    p.xu = a.hu;
     p.out = a.ye;
-    p.out_lo = nullptr;
     p.count = a.count + kW4Counters;
     p.clear = a.count;
     return run_gemv<W4_OUT>(m2, m2, p, a.group, sms, s);

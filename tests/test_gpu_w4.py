@@ -130,7 +130,7 @@ def run_ffn(dev, x, offsets, N, d, dff, group, act, R_cap, ws=None, stream=None)
     return y.cpu()
 
 
-H_STEP = 2.0 ** -8   # H in bf16; few rows keep a second part, which is only better
+H_STEP = 2.0 ** -8   # H in bf16 (many rows); few rows keep 16 bits, which is only better
 
 
 def check_ffn(W, x, y, offsets, group, act, rows=None):

@@ -43,13 +43,21 @@ def values(q, scale, group):
     return q * np.repeat(np.moveaxis(scale, -2, -1), group, axis=-1)[..., :K]
 
 
+def block_error(v):
+    """Few rows enter the products as 16-bit integers per block of 64 values: off by at most half a
+    unit, max / 32512 / 2 (1.1: the unit's and its reciprocal's own rounding)."""
+    pad = np.pad(np.abs(v), ((0, 0), (0, -v.shape[1] % 64)))
+    top = pad.reshape(v.shape[0], -1, 64).max(axis=2)
+    return np.repeat(top, 64, axis=1)[:, : v.shape[1]] * (1.1 / 65024)
+
+
 def ffn(x, w1, w3, w2, b1, b3, b2, act, h_step):
     """One expert on rows x (fp64): (y, error bound).  w [out, in] fp64.
 
     A product of K terms accumulated in fp32 is off by at most (K + 16) 2^-23 of
     the sum of its terms' magnitudes (every addition rounds or truncates by 2^-23
     at most; 16: the group scales and the sums over warps); h_step is H's
-    rounding (2^-8 for bf16, 2^-16 for two bf16 parts), y's is 2^-8.
+    rounding where it is kept in bf16 (2^-8), y's is 2^-8.
     |silu'| <= 1.1, |silu(u)| <= |u|, and its own evaluation 2^-20."""
     def product(x, w, b, dx):
         c = (w.shape[1] + 16) * 2.0 ** -23
@@ -57,15 +65,16 @@ def ffn(x, w1, w3, w2, b1, b3, b2, act, h_step):
         size = np.abs(x) @ np.abs(w).T + (0 if b is None else np.abs(b))
         return v, c * size + dx @ np.abs(w).T
 
-    zero = np.zeros_like(x)
-    u, du = product(x, w1, b1, zero)
+    dx = block_error(x)
+    u, du = product(x, w1, b1, dx)
     if act == "swiglu":
-        v, dv = product(x, w3, b3, zero)
+        v, dv = product(x, w3, b3, dx)
         silu = u / (1 + np.exp(-u))
         h = silu * v
         dh = 1.1 * du * (np.abs(v) + dv) + np.abs(silu) * dv + 2.0 ** -20 * np.abs(h)
     else:
         h, dh = np.maximum(u, 0), du
     dh = dh + h_step * (np.abs(h) + dh)
+    dh = dh + block_error(np.abs(h) + dh)
     y, dy = product(h, w2, b2, dh)
     return y, dy + 2.0 ** -8 * (np.abs(y) + dy)
