@@ -19,7 +19,7 @@
 // or TMEM, for a product that takes a few per cent of the time here.
 //
 // A CTA has four consumer warps and a producer warp.  Its tile is 128 weight rows
-// (64 features of W1 and the same of W3 for SwiGLU) by up to 16 tokens, a
+// (64 features of W1 and the same of W3 for SwiGLU) by up to 8 tokens, a
 // pipeline stage 256 of K: the producer brings the packed rows with TMA
 // (128-byte swizzle) and the tokens' rows and the group scales with cp.async
 // into an mbarrier ring.  A consumer warp owns 32 weight rows as two m16 tiles;
@@ -45,14 +45,13 @@ constexpr int kRows = 32 * kWarps;               // weight rows of a tile
 constexpr int kStageBlocks = 2;                  // 128-weight blocks of K per stage
 constexpr int kStageK = kStageBlocks * kW4Block;
 constexpr int kWBytes = kRows * kStageBlocks * kW4BlockBytes;   // 16 KB
-constexpr int kXBytes = 8 * kStageK;             // per 8 columns of bytes (4 tokens)
 constexpr int kOutPitch = kRows + 8;             // conflict-free accumulator writes
 constexpr int kMaxStages = 8;
 constexpr int kCtasPerSm = kWarps == 4 ? 3 : 2;
 constexpr int kSmem = kWarps == 4 ? 72 * 1024 : 110 * 1024;   // of a CTA
 constexpr int kBoxRows = 64, kBoxBytes = kBoxRows * 128;       // one TMA box of weights
 constexpr int kMinSteps = 2;                     // stages per CTA at least
-constexpr int kPartFloats = 16 * kRows;          // one fp32 part of a tile
+constexpr int kPartFloats = 8 * kRows;          // one fp32 part of a tile
 
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
 
@@ -92,7 +91,11 @@ __device__ __forceinline__ void mma_s8_first(int (&c)[4], uint32_t a0, uint32_t 
         : "=r"(c[0]), "=r"(c[1]), "=r"(c[2]), "=r"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(kMagic));
 }
-__device__ __forceinline__ float magic_sum(int c) { return __int_as_float(c) - 12582912.f; }
+constexpr float kMagicValue = 12582912.f;   // 1.5 2^23
+// kMagicValue + 256 hi + lo, rounded once to fp32
+__device__ __forceinline__ float joined(int hi, int lo) {
+    return fmaf(__int_as_float(hi) - kMagicValue, 256.f, __int_as_float(lo));
+}
 
 // (w ^ 0x88888888) & 0xF0F0F0F0: the odd nibbles as bytes 16 q
 __device__ __forceinline__ uint32_t odd_nibbles(uint32_t w) {
@@ -192,32 +195,36 @@ struct Cursor {
     }
 };
 
-template <int EPI, int G, int NT>
+template <int EPI, int G>
 struct Shape {
     static constexpr int MATS = EPI == W4_SWIGLU ? 2 : 1;
     static constexpr int FEATS = kRows / MATS;                   // output features of a tile
-    static constexpr int CHUNK = 4 * NT;                         // tokens of a tile, two columns each
     static constexpr int SGROUPS = kStageK / G;                  // groups per stage
-    static constexpr int X_OFF = kWBytes;
-    static constexpr int U_OFF = X_OFF + NT * kXBytes;           // units: 4 floats a token
-    static constexpr int S_OFF = U_OFF + CHUNK * 16;
-    static constexpr int STAGE = (S_OFF + SGROUPS * kRows * 2 + 1023) / 1024 * 1024;
-    static constexpr int OUT_BYTES = CHUNK * kOutPitch * 4;
+    static constexpr int S_OFF = kWBytes;                        // scales, behind the weights
+    static constexpr int U_OFF = S_OFF + SGROUPS * kRows * 2;    // units: 4 floats a token
 };
 
-template <int EPI, int G, int NT>
+// A launch's tiles hold up to `cap` (4 or 8) tokens, by its largest expert;
+// fewer make the stages smaller and their number larger.
+struct Ring {
+    uint32_t base;      // shared address
+    const uint8_t* ptr;
+    int cap, x_off, stage, stages;
+};
+
+template <int EPI, int G>
 __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* ma, const CUtensorMap* mb, Shared& sh,
-                                        uint32_t ring, int stages, const Plan& pl, const Waiter& w) {
-    using S = Shape<EPI, G, NT>;
+                                        const Ring& rg, const Plan& pl, const Waiter& w) {
+    using S = Shape<EPI, G>;
     const int lane = threadIdx.x & 31;
     const int ng = (p.k_dim + G - 1) / G;
     const int64_t padded = w4_padded(p.k_dim);
     // the rows of x, their units and the scales of the stage at c
     auto rows_of = [&](const Cursor& c, int st) {
         const int k0 = c.ks * kStageK;
-        const uint32_t base = ring + st * S::STAGE;
+        const uint32_t base = rg.base + st * rg.stage;
         // a token's 512 bytes: [block of 64][hi, lo][t][16], into [block][column][t][16]
-        const uint32_t xd = base + S::X_OFF + (lane >> 3) * (8 * NT * 64) + (lane >> 2 & 1) * 64 + (lane & 3) * 16;
+        const uint32_t xd = base + rg.x_off + (lane >> 3) * (rg.cap * 128) + (lane >> 2 & 1) * 64 + (lane & 3) * 16;
         const uint8_t* xs = p.x + ((int64_t)c.t.row0 * padded + k0) * 2 + lane * 16;
         for (int v = 0; v < c.t.n; ++v) cp16(xd + v * 128, xs + v * padded * 2, true);
         if (lane < c.t.n)
@@ -251,12 +258,12 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
     };
     uint32_t phase = 0, used = 0;
     for (int step = begin; step < end; ++step) {
-        if (!waited && pending == stages) catch_up();   // the ring is full of weights
+        if (!waited && pending == rg.stages) catch_up();   // the ring is full of weights
         ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.empty[stage]), phase ^ 1u, w));
         if (!ok) break;
         if (lane == 0) {
             const int kb = cur.ks * kStageBlocks * kW4BlockBytes;
-            const uint32_t fb = smem_u32(&sh.full[stage]), base = ring + stage * S::STAGE;
+            const uint32_t fb = smem_u32(&sh.full[stage]), base = rg.base + stage * rg.stage;
             const int row = cur.t.e * p.m_dim + cur.t.m0;
             constexpr int BOXES = kRows / kBoxRows, PER = BOXES / S::MATS;   // boxes of a matrix
             const int live = min(PER, (p.m_dim - cur.t.m0 + kBoxRows - 1) / kBoxRows);   // those that hold something
@@ -271,7 +278,7 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
         if (waited) rows_of(cur, stage);
         else ++pending;
         cur.next(sh, pl, S::FEATS);
-        if (++stage == stages) {
+        if (++stage == rg.stages) {
             stage = 0;
             phase ^= 1u;
         }
@@ -280,22 +287,103 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
     // nothing of this warp's copies is in flight when the CTA ends
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok && lane == 0) {   // aborted: the weights asked for last have landed too
-        for (int s = 0; s < stages; ++s)
+        for (int s = 0; s < rg.stages; ++s)
             if (used >> s & 1u)
                 drain_bar(smem_u32(&sh.full[s]), s < stage ? phase : phase ^ 1u, p.limit_ns, p.status);
     }
     __syncwarp();
 }
 
-template <int EPI, int G, int NT>
-__device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const uint8_t* ring, float* s_out, int stages,
-                                        const Plan& pl, const Waiter& w) {
-    using S = Shape<EPI, G, NT>;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+// This warp's part of steps [step, stop) of one tile of up to 4 NT tokens: the sums
+// into s_out[token][tile row].
+template <int EPI, int G, int UB, int NT>
+__device__ __forceinline__ void tile_sums(const GemvParams& p, Shared& sh, const Ring& rg, float* s_out, int step, int stop,
+                                          int kb0, int& stage, uint32_t& phase, bool& dead, const Waiter& w) {
+    using S = Shape<EPI, G>;
+    constexpr int JOIN = (G < UB ? G : UB) / 32;   // words whose sums join at once
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int nb = (p.k_dim + kW4Block - 1) / kW4Block, ng = (p.k_dim + G - 1) / G;
     const int pg = (g >> 1) | ((g & 1) << 2);   // tile row of mma row g: 0 4 1 5 2 6 3 7
     // m16 tile i of this warp: SwiGLU, the same 16 features of either matrix; else 32 rows
     auto tile_row = [&](int i) { return S::MATS == 2 ? i * S::FEATS + 16 * warp : 32 * warp + 16 * i; };
+    float acc[2][NT][2];   // [m16 tile][column block][row pg, pg + 8] of token 4 c + t
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) acc[i][c][0] = acc[i][c][1] = 0.f;
+    for (; step < stop; ++step, kb0 += kStageBlocks) {
+        // after an abort the warp only keeps the barriers going
+        if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(smem_u32(&sh.full[stage]), phase, w));
+        const uint8_t* base = rg.ptr + stage * rg.stage;
+#pragma unroll
+        for (int b = 0; b < kStageBlocks; ++b) {
+            if (dead || kb0 + b >= nb) break;   // a block past K holds nothing
+            uint4 wd[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    wd[i][h] = lds16(base + (tile_row(i) + 8 * h + pg) * 128 + (((4 * b + t) ^ pg) << 4));
+            int part[2][NT][4];
+            uint4 x[NT];   // a column that no token fills holds anything: it is not read back
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {   // 32 values
+                if (j % 2 == 0) {
+                    if ((kb0 + b) * kW4Block + j * 32 >= p.k_dim) break;
+#pragma unroll
+                    for (int c = 0; c < NT; ++c)
+                        x[c] = lds16(base + rg.x_off + ((2 * b + j / 2) * 2 * rg.cap + 8 * c + g) * 64 + t * 16);
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t w0 = word_of(wd[i][0], j), w1 = word_of(wd[i][1], j);
+                    const uint32_t a0 = odd_nibbles(w0 << 4), a1 = odd_nibbles(w1 << 4);
+                    const uint32_t a2 = odd_nibbles(w0), a3 = odd_nibbles(w1);
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        const uint32_t b0 = j % 2 ? x[c].z : x[c].x, b1 = j % 2 ? x[c].w : x[c].y;
+                        if (j % JOIN == 0) mma_s8_first(part[i][c], a0, a1, a2, a3, b0, b1);
+                        else mma_s8(part[i][c], a0, a1, a2, a3, b0, b1);
+                    }
+                }
+                // the sums of JOIN x 32 values join: 256 hi + lo, times the unit and the scale
+                const bool end = JOIN == 4 ? j == 3 || (j == 1 && (kb0 + b) * kW4Block + 64 >= p.k_dim) : (j + 1) % JOIN == 0;
+                const int gi = b * (kW4Block / G) + j * (kW4Block / G) / 4;   // group of the stage
+                if (!end || kb0 * (kW4Block / G) + gi >= ng) continue;        // (a last block shorter than 64)
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    const float un = *reinterpret_cast<const float*>(base + S::U_OFF + (4 * c + t) * 16 + (2 * b + j / 2) * 4);
+                    const float off = -kMagicValue * un;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint8_t* sa = base + S::S_OFF + (gi * kRows + tile_row(i) + pg) * 2;
+                        acc[i][c][0] = fmaf(fmaf(joined(part[i][c][0], part[i][c][1]), un, off), lds_bf16(sa), acc[i][c][0]);
+                        acc[i][c][1] = fmaf(fmaf(joined(part[i][c][2], part[i][c][3]), un, off), lds_bf16(sa + 16), acc[i][c][1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));
+        if (++stage == rg.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+    }
+    named_bar(1, kRows);   // the previous tile's values have been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) s_out[(4 * c + t) * kOutPitch + tile_row(i) + pg + 8 * r] = acc[i][c][r];
+}
+
+template <int EPI, int G, int UB>
+__device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const Ring& rg, float* s_out, const Plan& pl,
+                                        const Waiter& w) {
+    using S = Shape<EPI, G>;
+    const int tid = threadIdx.x;
     int stage = 0;
     uint32_t phase = 0;
     bool dead = false;
@@ -305,89 +393,10 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
         const int u = step / pl.steps, u0 = u * pl.steps, u1 = u0 + pl.steps;
         const int stop = min(end, u1);
         const Unit un = unit_of(sh, pl, u, S::FEATS);
-        float acc[2][NT][2];   // [m16 tile][column block][row pg, pg + 8] of token 4 c + t
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < NT; ++c) acc[i][c][0] = acc[i][c][1] = 0.f;
-        const int from = step;
-        for (; step < stop; ++step) {
-            // after an abort the warp only keeps the barriers going
-            if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(smem_u32(&sh.full[stage]), phase, w));
-            const uint8_t* base = ring + stage * S::STAGE;
-            const int kb0 = (step - u0) * kStageBlocks;
-            float4 unit[NT];
-#pragma unroll
-            for (int c = 0; c < NT; ++c) unit[c] = *reinterpret_cast<const float4*>(base + S::U_OFF + (4 * c + t) * 16);
-#pragma unroll
-            for (int b = 0; b < kStageBlocks; ++b) {
-                if (dead || kb0 + b >= nb) break;   // a block past K holds nothing
-                uint4 wd[2][2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        wd[i][h] = lds16(base + (tile_row(i) + 8 * h + pg) * 128 + (((4 * b + t) ^ pg) << 4));
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {   // blocks of 64 values
-                    if ((kb0 + b) * kW4Block + q * kW4ActBlock >= p.k_dim) break;
-                    uint4 x[NT];   // a column that no token fills holds anything: it is not read back
-#pragma unroll
-                    for (int c = 0; c < NT; ++c)
-                        x[c] = lds16(base + S::X_OFF + ((2 * b + q) * 8 * NT + 8 * c + g) * 64 + t * 16);
-                    int part[2][NT][4];
-#pragma unroll
-                    for (int jj = 0; jj < 2; ++jj) {
-                        const int j = 2 * q + jj;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t w0 = word_of(wd[i][0], j), w1 = word_of(wd[i][1], j);
-                            const uint32_t a0 = odd_nibbles(w0 << 4), a1 = odd_nibbles(w1 << 4);
-                            const uint32_t a2 = odd_nibbles(w0), a3 = odd_nibbles(w1);
-#pragma unroll
-                            for (int c = 0; c < NT; ++c) {
-                                const uint32_t b0 = jj ? x[c].z : x[c].x, b1 = jj ? x[c].w : x[c].y;
-                                if (jj == 0 || G == 32) mma_s8_first(part[i][c], a0, a1, a2, a3, b0, b1);
-                                else mma_s8(part[i][c], a0, a1, a2, a3, b0, b1);
-                            }
-                        }
-                        if (jj == 0 && G > 32) continue;
-                        // the block's (or group's) sums join: 256 hi + lo, times the unit and the scale
-                        const int gi = b * (kW4Block / G) + j * (kW4Block / G) / 4;   // group of the stage
-                        if (kb0 * (kW4Block / G) + gi >= ng) continue;                // a last block shorter than 64
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint8_t* sa = base + S::S_OFF + (gi * kRows + tile_row(i) + pg) * 2;
-                            const float f0 = lds_bf16(sa), f1 = lds_bf16(sa + 16);
-#pragma unroll
-                            for (int c = 0; c < NT; ++c) {
-                                const int qi = 2 * b + q;
-                                const float un64 = qi == 0 ? unit[c].x : qi == 1 ? unit[c].y : qi == 2 ? unit[c].z : unit[c].w;
-                                const int* pt = part[i][c];
-                                const float v0 = fmaf(magic_sum(pt[0]), 256.f, magic_sum(pt[1])) * un64;
-                                const float v1 = fmaf(magic_sum(pt[2]), 256.f, magic_sum(pt[3])) * un64;
-                                acc[i][c][0] = fmaf(v0, f0, acc[i][c][0]);
-                                acc[i][c][1] = fmaf(v1, f1, acc[i][c][1]);
-                            }
-                        }
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.empty[stage]));
-            if (++stage == stages) {
-                stage = 0;
-                phase ^= 1u;
-            }
-        }
-        // accumulators -> s_out[token][tile row]
-        named_bar(1, kRows);   // the previous tile's values have been read
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < NT; ++c)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) s_out[(4 * c + t) * kOutPitch + tile_row(i) + pg + 8 * r] = acc[i][c][r];
+        const int from = step, kb0 = (step - u0) * kStageBlocks;
+        if (un.n <= 4) tile_sums<EPI, G, UB, 1>(p, sh, rg, s_out, step, stop, kb0, stage, phase, dead, w);
+        else tile_sums<EPI, G, UB, 2>(p, sh, rg, s_out, step, stop, kb0, stage, phase, dead, w);
+        step = stop;
         named_bar(1, kRows);
         if (from > u0 || stop < u1) {   // other CTAs hold the rest of the tile's K
             const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u1 - 1);
@@ -435,9 +444,9 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
             s_out[col * kOutPitch + f] = in ? o : 0.f;
         }
         if (EPI == W4_OUT) continue;
-        // H as integers: eight lanes per token and block of 64 features
+        // H as integers: eight lanes per token and 64 features
         named_bar(1, kRows);
-        constexpr int BLOCKS = S::FEATS / kW4ActBlock;
+        constexpr int BLOCKS = S::FEATS / kW4ActBlock, HUB = EPI == W4_RELU && G == 128 ? 128 : 64;
         const int64_t padded = w4_padded(p.m_dim);
         for (int k0 = 0; k0 < un.n * BLOCKS; k0 += kRows / 8) {
             const int k = k0 + tid / 8, l = tid % 8;
@@ -454,7 +463,7 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int o = HUB / 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
             float unit16, inv;
             block_unit(m, unit16, inv);
             uint2 hi, lo;
@@ -470,8 +479,10 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const u
     }
 }
 
-// Rows of x as integers: eight lanes per block of 64 values.
+// Rows of x as integers: eight lanes per 64 values, whose unit is that of their
+// block of UB (64 or 128).
 constexpr int kRowThreads = 256;
+template <int UB>
 __global__ void __launch_bounds__(kRowThreads)
 w4_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ offsets, int N, int64_t R_cap, int k_dim,
                uint8_t* __restrict__ xq, float* __restrict__ xu) {
@@ -479,7 +490,7 @@ w4_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ 
     pdl_launch();
     const int64_t last = offsets[N], rows = last < 0 ? 0 : (last > R_cap ? R_cap : last);
     const int64_t padded = w4_padded(k_dim);
-    const int blocks = (k_dim + kW4ActBlock - 1) / kW4ActBlock, l = threadIdx.x & 7;
+    const int blocks = (int)(padded / kW4ActBlock), l = threadIdx.x & 7;
     for (int64_t q0 = (int64_t)blockIdx.x * (kRowThreads / 8); q0 < rows * blocks; q0 += (int64_t)gridDim.x * (kRowThreads / 8)) {
         const int64_t q = q0 + threadIdx.x / 8, row = q / blocks;
         const int k = (int)(q - row * blocks) * kW4ActBlock + 8 * l;
@@ -494,7 +505,7 @@ w4_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ 
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        for (int o = UB / 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         float unit16, inv;
         block_unit(m, unit16, inv);
         uint2 hi, lo;
@@ -509,13 +520,20 @@ w4_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ 
     }
 }
 
-template <int EPI, int G, int NT>
+template <int EPI, int G, int UB>
 __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap* ma, const CUtensorMap* mb, Shared& sh,
-                                          uint8_t* smem) {
-    using S = Shape<EPI, G, NT>;
+                                          uint8_t* smem, int most) {
+    using S = Shape<EPI, G>;
     const int tid = threadIdx.x;
+    Ring rg;
+    rg.cap = most <= 4 ? 4 : 8;
+    rg.x_off = (S::U_OFF + rg.cap * 16 + 127) / 128 * 128;
+    rg.stage = (rg.x_off + rg.cap * 2 * kStageK + 1023) / 1024 * 1024;
+    rg.stages = min(kMaxStages, (p.smem_bytes - 1024 - rg.cap * kOutPitch * 4) / rg.stage);
+    rg.base = smem_u32(smem);
+    rg.ptr = smem;
     Plan pl;
-    pl.chunk = S::CHUNK;
+    pl.chunk = rg.cap;
     pl.tiles = (p.m_dim + S::FEATS - 1) / S::FEATS;
     pl.steps = (p.k_dim + kStageK - 1) / kStageK;
     if (tid < 32) {   // live experts and their first units: four experts a lane, a scan over the lanes
@@ -525,7 +543,7 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
             const int e = 4 * tid + i;
             n[i] = e < p.N ? max(0, sh.row[e + 1] - sh.row[e]) : 0;
             live += n[i] > 0;
-            units += (n[i] + S::CHUNK - 1) / S::CHUNK * pl.tiles;
+            units += (n[i] + rg.cap - 1) / rg.cap * pl.tiles;
         }
         int l = live, u = units;
 #pragma unroll
@@ -547,7 +565,7 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
             if (n[i] > 0) {
                 sh.exp[l] = 4 * tid + i;
                 sh.first[l++] = u;
-                u += (n[i] + S::CHUNK - 1) / S::CHUNK * pl.tiles;
+                u += (n[i] + rg.cap - 1) / rg.cap * pl.tiles;
             }
     }
     __syncthreads();
@@ -559,19 +577,18 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
         pdl_launch();
         return;
     }
-    const int stages = min(kMaxStages, (p.smem_bytes - 1024 - S::OUT_BYTES) / S::STAGE);
-    float* s_out = reinterpret_cast<float*>(smem + stages * S::STAGE);
+    float* s_out = reinterpret_cast<float*>(smem + rg.stages * rg.stage);
     const Waiter w{&sh.abort, p.status, p.limit_ns};
     if (tid >= 32 * kWarps) {
-        produce<EPI, G, NT>(p, ma, mb, sh, smem_u32(smem), stages, pl, w);
+        produce<EPI, G>(p, ma, mb, sh, rg, pl, w);
     } else {
         pdl_wait();
         pdl_launch();
-        consume<EPI, G, NT>(p, sh, smem, s_out, stages, pl, w);
+        consume<EPI, G, UB>(p, sh, rg, s_out, pl, w);
     }
 }
 
-template <int EPI, int G>
+template <int EPI, int G, int UB>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const GemvParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -602,9 +619,7 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     __syncthreads();
     const int most = s_most;
     if (most > 0) {
-        if (most <= 4) run_tiles<EPI, G, 1>(p, &map_a, &map_b, sh, smem);
-        else if (most <= 8) run_tiles<EPI, G, 2>(p, &map_a, &map_b, sh, smem);
-        else run_tiles<EPI, G, 4>(p, &map_a, &map_b, sh, smem);
+        run_tiles<EPI, G, UB>(p, &map_a, &map_b, sh, smem, most);
     } else {
         pdl_wait();
         pdl_launch();
@@ -620,9 +635,9 @@ bool make_map_w4(CUtensorMap* map, const void* q, int64_t rows, int64_t pitch) {
     return make_map_u8(map, q, rows, pitch, kBoxRows);
 }
 
-template <int EPI, int G>
+template <int EPI, int G, int UB>
 cudaError_t run_gemv_g(const CUtensorMap& a, const CUtensorMap& b, GemvParams p, int sms, cudaStream_t s) {
-    auto kern = w4_gemv_kernel<EPI, G>;
+    auto kern = w4_gemv_kernel<EPI, G, UB>;
     cudaError_t err = once_per_device(reinterpret_cast<const void*>(kern), [](const void* k) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     });
@@ -631,11 +646,13 @@ cudaError_t run_gemv_g(const CUtensorMap& a, const CUtensorMap& b, GemvParams p,
     return launch_k(kern, dim3((unsigned)w4_gemv_ctas(sms)), dim3(kThreads), kSmem, s, 1, a, b, p);
 }
 
-template <int EPI>
+// Groups of 128: one unit per 128 values and one join per group, except for the H
+// of SwiGLU, whose tiles have 64 features.
+template <int EPI, int UB128>
 cudaError_t run_gemv(const CUtensorMap& a, const CUtensorMap& b, const GemvParams& p, int group, int sms, cudaStream_t s) {
-    if (group == 32) return run_gemv_g<EPI, 32>(a, b, p, sms, s);
-    if (group == 64) return run_gemv_g<EPI, 64>(a, b, p, sms, s);
-    return run_gemv_g<EPI, 128>(a, b, p, sms, s);
+    if (group == 32) return run_gemv_g<EPI, 32, 64>(a, b, p, sms, s);
+    if (group == 64) return run_gemv_g<EPI, 64, 64>(a, b, p, sms, s);
+    return run_gemv_g<EPI, 128, UB128>(a, b, p, sms, s);
 }
 
 }  // namespace
@@ -674,12 +691,13 @@ cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     p.hu = a.hu;
     p.count = a.count;
     p.clear = a.count + kW4Counters;
-    const int64_t row_blocks = (a.R_cap * ((a.d + kW4ActBlock - 1) / kW4ActBlock) + kRowThreads / 8 - 1) / (kRowThreads / 8);
-    err = launch_k(w4_rows_kernel, dim3((unsigned)(row_blocks < 8 * sms ? row_blocks : 8 * sms)), dim3(kRowThreads), 0, s, 1,
-                   a.xe, a.offsets, a.N, a.R_cap, a.d, a.xq, a.xu);
+    const int64_t row_blocks = (a.R_cap * (w4_padded(a.d) / kW4ActBlock) + kRowThreads / 8 - 1) / (kRowThreads / 8);
+    err = launch_k(a.group == 128 ? w4_rows_kernel<128> : w4_rows_kernel<64>,
+                   dim3((unsigned)(row_blocks < 8 * sms ? row_blocks : 8 * sms)), dim3(kRowThreads), 0, s, 1, a.xe, a.offsets,
+                   a.N, a.R_cap, a.d, a.xq, a.xu);
     if (err != cudaSuccess) return err;
-    err = a.act == MOE_SWIGLU ? run_gemv<W4_SWIGLU>(m1, m3, p, a.group, sms, s)
-                              : run_gemv<W4_RELU>(m1, m3, p, a.group, sms, s);
+    err = a.act == MOE_SWIGLU ? run_gemv<W4_SWIGLU, 128>(m1, m3, p, a.group, sms, s)
+                              : run_gemv<W4_RELU, 128>(m1, m3, p, a.group, sms, s);
     if (err != cudaSuccess) return err;
     p.m_dim = a.d;
     p.k_dim = a.d_ff;
@@ -691,7 +709,8 @@ cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     p.out = a.ye;
     p.count = a.count + kW4Counters;
     p.clear = a.count;
-    return run_gemv<W4_OUT>(m2, m2, p, a.group, sms, s);
+    return a.act == MOE_SWIGLU ? run_gemv<W4_OUT, 64>(m2, m2, p, a.group, sms, s)
+                               : run_gemv<W4_OUT, 128>(m2, m2, p, a.group, sms, s);
 }
 
 }  // namespace moe

@@ -44,11 +44,11 @@ def values(q, scale, group):
 
 
 def block_error(v):
-    """Few rows enter the products as 16-bit integers per block of 64 values: off by at most half a
+    """Few rows enter the products as 16-bit integers per block of 64 or 128 values: off by at most half a
     unit, max / 32512 / 2 (1.1: the unit's and its reciprocal's own rounding)."""
-    pad = np.pad(np.abs(v), ((0, 0), (0, -v.shape[1] % 64)))
-    top = pad.reshape(v.shape[0], -1, 64).max(axis=2)
-    return np.repeat(top, 64, axis=1)[:, : v.shape[1]] * (1.1 / 65024)
+    pad = np.pad(np.abs(v), ((0, 0), (0, -v.shape[1] % 128)))
+    top = pad.reshape(v.shape[0], -1, 128).max(axis=2)
+    return np.repeat(top, 128, axis=1)[:, : v.shape[1]] * (1.1 / 65024)
 
 
 def ffn(x, w1, w3, w2, b1, b3, b2, act, h_step):
