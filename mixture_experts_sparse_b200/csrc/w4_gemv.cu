@@ -27,11 +27,10 @@
 // row group reads tile row perm(g): rows 0 4 1 5 2 6 3 7, whose swizzled 16-byte
 // chunks fall into different banks.
 //
-// The pipeline stages of all tiles form one list, cut into equal ranges, one per
-// CTA, so that every SM streams the same number of bytes whatever the sizes.  A
-// tile that two or more CTAs share is added up by the one that arrives last,
-// from fp32 parts in the workspace, in K order: the result depends on where the
-// cuts fall (on the live experts and rows), not on the order of arrival.
+// CTAs take whole tiles, or equal ranges of the list of all tiles' stages.  A tile
+// that such a cut divides is added up by the CTA that arrives last, from fp32 parts
+// in the workspace, in K order: the result depends on where the cuts fall (on
+// the number of tiles), not on the order of arrival.
 #include "tc_common.cuh"
 #include "w4.cuh"
 
@@ -50,7 +49,8 @@ constexpr int kMaxStages = 8;
 constexpr int kCtasPerSm = kWarps == 4 ? 3 : 2;
 constexpr int kSmem = kWarps == 4 ? 72 * 1024 : 110 * 1024;   // of a CTA
 constexpr int kBoxRows = 64, kBoxBytes = kBoxRows * 128;       // one TMA box of weights
-constexpr int kMinSteps = 2;                     // stages per CTA at least
+constexpr int kMinSteps = 2;                     // stages per CTA at least, when they are dealt out
+constexpr int kIdleSteps = 8;                    // see the plan
 constexpr int kPartFloats = 8 * kRows;          // one fp32 part of a tile
 
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
@@ -145,17 +145,26 @@ struct Shared {
     int row[129];
     int exp[128];      // live experts
     int first[129];    // their first unit
-    int live, abort, last;
+    int live, cap, abort, last;
 };
 
-// The list of a launch: units (live expert, feature tile, row chunk), each of
-// `steps` pipeline stages.
+// The work of a launch: units (live expert, feature tile, row chunk), each of
+// `steps` pipeline stages.  CTA b takes the units b, b + gridDim.x, ...; or (deal)
+// the stages of all units form one list, cut into equal ranges, one per CTA.
 struct Plan {
     int tiles, steps, chunk;   // feature tiles; stages per unit; rows per chunk
-    int units, total;          // total = units * steps
-    int ctas;
-    __device__ int begin(int c) const { return (int)((int64_t)total * c / ctas); }
-    __device__ int cta_of(int step) const { return (int)(((int64_t)(step + 1) * ctas - 1) / total); }
+    int units;
+    bool deal;
+    int ctas, each, rest;      // deal: CTAs with a range; stages / ctas and what is left over
+    __device__ int begin(int c) const {   // floor(stages c / ctas) in 32 bits (c, ctas < 2^10)
+        return c >= ctas ? units * steps : each * c + rest * c / ctas;
+    }
+    __device__ int cta_of(int step) const {   // the CTA that holds this stage
+        int c = (int)((float)step * ((float)ctas / (float)(units * steps)));
+        while (begin(c) > step) --c;
+        while (begin(c + 1) <= step) ++c;
+        return c;
+    }
 };
 
 struct Unit {
@@ -179,19 +188,33 @@ __device__ __forceinline__ Unit unit_of(const Shared& sh, const Plan& pl, int u,
     return t;
 }
 
-// A position in the list.
-struct Cursor {
-    int u, ks;
-    Unit t;
-    __device__ void start(const Shared& sh, const Plan& pl, int step, int feats) {
-        u = step / pl.steps;
-        ks = step - u * pl.steps;
-        t = unit_of(sh, pl, u, feats);
+// A CTA's way through its work, segment by segment: stages [k0, k1) of unit u.
+struct Walk {
+    int u, k0, k1, left;   // deal: the stages after this segment
+    __device__ void start(const Plan& pl) {
+        k0 = 0;
+        if (pl.deal) {
+            const int b = pl.begin(blockIdx.x);
+            left = pl.begin(blockIdx.x + 1) - b;
+            u = b / pl.steps;
+            k1 = b - u * pl.steps;   // next() goes on from here
+            --u;
+        } else {
+            u = (int)blockIdx.x - (int)gridDim.x;
+            k1 = pl.steps;
+        }
     }
-    __device__ void next(const Shared& sh, const Plan& pl, int feats) {
-        if (++ks < pl.steps) return;
-        ks = 0;
-        if (++u < pl.units) t = unit_of(sh, pl, u, feats);
+    __device__ bool next(const Plan& pl) {
+        if (!pl.deal) {
+            u += gridDim.x;
+            return u < pl.units;
+        }
+        if (left == 0) return false;
+        ++u;
+        k0 = k1 == pl.steps ? 0 : k1;
+        k1 = min(pl.steps, k0 + left);
+        left -= k1 - k0;
+        return true;
     }
 };
 
@@ -219,68 +242,69 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
     const int lane = threadIdx.x & 31;
     const int ng = (p.k_dim + G - 1) / G;
     const int64_t padded = w4_padded(p.k_dim);
-    // the rows of x, their units and the scales of the stage at c
-    auto rows_of = [&](const Cursor& c, int st) {
-        const int k0 = c.ks * kStageK;
+    // the rows of x, their units and the scales of stage ks of tile c
+    auto rows_of = [&](const Unit& c, int ks, int st) {
+        const int k0 = ks * kStageK;
         const uint32_t base = rg.base + st * rg.stage;
         // a token's 512 bytes: [block of 64][hi, lo][t][16], into [block][column][t][16]
         const uint32_t xd = base + rg.x_off + (lane >> 3) * (rg.cap * 128) + (lane >> 2 & 1) * 64 + (lane & 3) * 16;
-        const uint8_t* xs = p.x + ((int64_t)c.t.row0 * padded + k0) * 2 + lane * 16;
-        for (int v = 0; v < c.t.n; ++v) cp16(xd + v * 128, xs + v * padded * 2, true);
-        if (lane < c.t.n)
-            cp16(base + S::U_OFF + lane * 16, p.xu + ((int64_t)(c.t.row0 + lane) * padded + k0) / kW4ActBlock, true);
+        const uint8_t* xs = p.x + ((int64_t)c.row0 * padded + k0) * 2 + lane * 16;
+        for (int v = 0; v < c.n; ++v) cp16(xd + v * 128, xs + v * padded * 2, true);
+        if (lane < c.n)
+            cp16(base + S::U_OFF + lane * 16, p.xu + ((int64_t)(c.row0 + lane) * padded + k0) / kW4ActBlock, true);
         // scales: 8 tile rows a lane
         constexpr int LANES = kRows / 8;
         const int r = lane % LANES * 8;       // tile row
         const uint16_t* sc = S::MATS == 2 && r >= S::FEATS ? p.sb : p.sa;
-        const int f = c.t.m0 + (S::MATS == 2 ? r % S::FEATS : r);
+        const int f = c.m0 + (S::MATS == 2 ? r % S::FEATS : r);
 #pragma unroll
         for (int i = 0; i < S::SGROUPS; i += 32 / LANES) {
             const int gi = i + lane / LANES, g = k0 / G + gi;
             const bool have = g < ng && f < p.m_dim;
-            cp16(base + S::S_OFF + gi * kRows * 2 + r * 2, have ? sc + ((int64_t)c.t.e * ng + g) * p.m_dim + f : p.sa, have);
+            cp16(base + S::S_OFF + gi * kRows * 2 + r * 2, have ? sc + ((int64_t)c.e * ng + g) * p.m_dim + f : p.sa, have);
         }
         cp_arrive(smem_u32(&sh.full[st]));
     };
-    const int begin = pl.begin(blockIdx.x), end = pl.begin(blockIdx.x + 1);
-    Cursor cur;
-    cur.start(sh, pl, begin, S::FEATS);
-    Cursor late = cur;               // the first stages' rows, asked for after the wait
+    Walk walk, late;                 // late: the first stages' rows, asked for after the wait
+    walk.start(pl);
+    late = walk;
     int pending = 0, stage = 0;
     bool waited = false, ok = true;
     auto catch_up = [&]() {
         pdl_wait();
         waited = true;
-        for (int i = 0; i < pending; ++i) {
-            rows_of(late, i);
-            late.next(sh, pl, S::FEATS);
+        for (int i = 0; i < pending && late.next(pl);) {
+            const Unit t = unit_of(sh, pl, late.u, S::FEATS);
+            for (int ks = late.k0; ks < late.k1 && i < pending; ++ks, ++i) rows_of(t, ks, i);
         }
     };
     uint32_t phase = 0, used = 0;
-    for (int step = begin; step < end; ++step) {
-        if (!waited && pending == rg.stages) catch_up();   // the ring is full of weights
-        ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.empty[stage]), phase ^ 1u, w));
-        if (!ok) break;
-        if (lane == 0) {
-            const int kb = cur.ks * kStageBlocks * kW4BlockBytes;
-            const uint32_t fb = smem_u32(&sh.full[stage]), base = rg.base + stage * rg.stage;
-            const int row = cur.t.e * p.m_dim + cur.t.m0;
-            constexpr int BOXES = kRows / kBoxRows, PER = BOXES / S::MATS;   // boxes of a matrix
-            const int live = min(PER, (p.m_dim - cur.t.m0 + kBoxRows - 1) / kBoxRows);   // those that hold something
-            mbar_expect_tx(fb, live * S::MATS * kBoxBytes);
+    while (ok && walk.next(pl)) {
+        const Unit t = unit_of(sh, pl, walk.u, S::FEATS);
+        constexpr int BOXES = kRows / kBoxRows, PER = BOXES / S::MATS;           // boxes of a matrix
+        const int live = min(PER, (p.m_dim - t.m0 + kBoxRows - 1) / kBoxRows);   // those that hold something
+        const int row = t.e * p.m_dim + t.m0;
+        for (int ks = walk.k0; ks < walk.k1; ++ks) {
+            if (!waited && pending == rg.stages) catch_up();   // the ring is full of weights
+            ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.empty[stage]), phase ^ 1u, w));
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t fb = smem_u32(&sh.full[stage]), base = rg.base + stage * rg.stage;
+                mbar_expect_tx(fb, live * S::MATS * kBoxBytes);
 #pragma unroll
-            for (int b = 0; b < BOXES; ++b)
-                if (b % PER < live)
-                    tma_load_2d(base + b * kBoxBytes, b < PER ? ma : mb, fb, kb, row + b % PER * kBoxRows);
-        }
-        __syncwarp();
-        used |= 1u << stage;
-        if (waited) rows_of(cur, stage);
-        else ++pending;
-        cur.next(sh, pl, S::FEATS);
-        if (++stage == rg.stages) {
-            stage = 0;
-            phase ^= 1u;
+                for (int b = 0; b < BOXES; ++b)
+                    if (b % PER < live)
+                        tma_load_2d(base + b * kBoxBytes, b < PER ? ma : mb, fb, ks * kStageBlocks * kW4BlockBytes,
+                                    row + b % PER * kBoxRows);
+            }
+            __syncwarp();
+            used |= 1u << stage;
+            if (waited) rows_of(t, ks, stage);
+            else ++pending;
+            if (++stage == rg.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
         }
     }
     if (!waited) catch_up();
@@ -294,11 +318,11 @@ __device__ __forceinline__ void produce(const GemvParams& p, const CUtensorMap* 
     __syncwarp();
 }
 
-// This warp's part of steps [step, stop) of one tile of up to 4 NT tokens: the sums
+// This warp's part of stages [ks, stop) of one tile of up to 4 NT tokens: the sums
 // into s_out[token][tile row].
 template <int EPI, int G, int UB, int NT>
-__device__ __forceinline__ void tile_sums(const GemvParams& p, Shared& sh, const Ring& rg, float* s_out, int step, int stop,
-                                          int kb0, int& stage, uint32_t& phase, bool& dead, const Waiter& w) {
+__device__ __forceinline__ void tile_sums(const GemvParams& p, Shared& sh, const Ring& rg, float* s_out, int ks, int stop,
+                                          int& stage, uint32_t& phase, bool& dead, const Waiter& w) {
     using S = Shape<EPI, G>;
     constexpr int JOIN = (G < UB ? G : UB) / 32;   // words whose sums join at once
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -311,7 +335,8 @@ __device__ __forceinline__ void tile_sums(const GemvParams& p, Shared& sh, const
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int c = 0; c < NT; ++c) acc[i][c][0] = acc[i][c][1] = 0.f;
-    for (; step < stop; ++step, kb0 += kStageBlocks) {
+    for (; ks < stop; ++ks) {
+        const int kb0 = ks * kStageBlocks;
         // after an abort the warp only keeps the barriers going
         if (!dead) dead = !__all_sync(0xffffffffu, wait_bar(smem_u32(&sh.full[stage]), phase, w));
         const uint8_t* base = rg.ptr + stage * rg.stage;
@@ -387,20 +412,17 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const R
     int stage = 0;
     uint32_t phase = 0;
     bool dead = false;
-    int step = pl.begin(blockIdx.x);
-    const int end = pl.begin(blockIdx.x + 1);
-    while (step < end) {
-        const int u = step / pl.steps, u0 = u * pl.steps, u1 = u0 + pl.steps;
-        const int stop = min(end, u1);
-        const Unit un = unit_of(sh, pl, u, S::FEATS);
-        const int from = step, kb0 = (step - u0) * kStageBlocks;
-        if (un.n <= 4) tile_sums<EPI, G, UB, 1>(p, sh, rg, s_out, step, stop, kb0, stage, phase, dead, w);
-        else tile_sums<EPI, G, UB, 2>(p, sh, rg, s_out, step, stop, kb0, stage, phase, dead, w);
-        step = stop;
+    Walk walk;
+    walk.start(pl);
+    while (walk.next(pl)) {
+        const Unit un = unit_of(sh, pl, walk.u, S::FEATS);
+        if (un.n <= 4) tile_sums<EPI, G, UB, 1>(p, sh, rg, s_out, walk.k0, walk.k1, stage, phase, dead, w);
+        else tile_sums<EPI, G, UB, 2>(p, sh, rg, s_out, walk.k0, walk.k1, stage, phase, dead, w);
         named_bar(1, kRows);
-        if (from > u0 || stop < u1) {   // other CTAs hold the rest of the tile's K
-            const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u1 - 1);
-            float* dst = p.part + ((int64_t)blockIdx.x * 2 + (from > u0 ? 0 : 1)) * kPartFloats;
+        if (walk.k1 - walk.k0 < pl.steps) {   // other CTAs hold the rest of the tile's K
+            const int u0 = walk.u * pl.steps;
+            const int c0 = pl.cta_of(u0), c1 = pl.cta_of(u0 + pl.steps - 1);
+            float* dst = p.part + ((int64_t)blockIdx.x * 2 + (walk.k0 > 0 ? 0 : 1)) * kPartFloats;
             for (int col = 0; col < un.n; ++col) __stcg(dst + col * kRows + tid, s_out[col * kOutPitch + tid]);
             named_bar(1, kRows);
             if (tid == 0) {   // the barrier orders the CTA's stores before this thread's fence
@@ -522,28 +544,26 @@ w4_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ 
 
 template <int EPI, int G, int UB>
 __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap* ma, const CUtensorMap* mb, Shared& sh,
-                                          uint8_t* smem, int most) {
+                                          uint8_t* smem) {
     using S = Shape<EPI, G>;
     const int tid = threadIdx.x;
-    Ring rg;
-    rg.cap = most <= 4 ? 4 : 8;
-    rg.x_off = (S::U_OFF + rg.cap * 16 + 127) / 128 * 128;
-    rg.stage = (rg.x_off + rg.cap * 2 * kStageK + 1023) / 1024 * 1024;
-    rg.stages = min(kMaxStages, (p.smem_bytes - 1024 - rg.cap * kOutPitch * 4) / rg.stage);
-    rg.base = smem_u32(smem);
-    rg.ptr = smem;
     Plan pl;
-    pl.chunk = rg.cap;
     pl.tiles = (p.m_dim + S::FEATS - 1) / S::FEATS;
     pl.steps = (p.k_dim + kStageK - 1) / kStageK;
     if (tid < 32) {   // live experts and their first units: four experts a lane, a scan over the lanes
-        int n[4], live = 0, units = 0;
+        int n[4], live = 0, units = 0, most = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = 4 * tid + i;
             n[i] = e < p.N ? max(0, sh.row[e + 1] - sh.row[e]) : 0;
+            most = max(most, n[i]);
+        }
+        most = __reduce_max_sync(0xffffffffu, most);
+        const int cap = most <= 4 ? 4 : 8;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
             live += n[i] > 0;
-            units += (n[i] + rg.cap - 1) / rg.cap * pl.tiles;
+            units += (n[i] + cap - 1) / cap * pl.tiles;
         }
         int l = live, u = units;
 #pragma unroll
@@ -557,6 +577,7 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
         if (tid == 31) {
             sh.live = l;
             sh.first[l] = u;
+            sh.cap = cap;
         }
         l -= live;
         u -= units;
@@ -565,14 +586,30 @@ __device__ __forceinline__ void run_tiles(const GemvParams& p, const CUtensorMap
             if (n[i] > 0) {
                 sh.exp[l] = 4 * tid + i;
                 sh.first[l++] = u;
-                u += (n[i] + rg.cap - 1) / rg.cap * pl.tiles;
+                u += (n[i] + cap - 1) / cap * pl.tiles;
             }
     }
     __syncthreads();
+    Ring rg;
+    rg.cap = sh.cap;
+    rg.x_off = (S::U_OFF + rg.cap * 16 + 127) / 128 * 128;
+    rg.stage = (rg.x_off + rg.cap * 2 * kStageK + 1023) / 1024 * 1024;
+    rg.stages = min(kMaxStages, (p.smem_bytes - 1024 - rg.cap * kOutPitch * 4) / rg.stage);
+    rg.base = smem_u32(smem);
+    rg.ptr = smem;
+    pl.chunk = rg.cap;
     pl.units = sh.first[sh.live];
-    pl.total = pl.units * pl.steps;
-    pl.ctas = min((pl.total + kMinSteps - 1) / kMinSteps, (int)gridDim.x);
-    if ((int)blockIdx.x >= pl.ctas) {
+    // Whole units leave CTAs idle in the last wave; dealing out stages costs the
+    // shared tiles' parts.  The former while it idles less than kIdleSteps stages
+    // per CTA: with 2 the 32 ReLU experts (16 stages, 0.42 of the CTAs idle) took
+    // 59 us and not 52, the odd sizes 22.7 and not 21.7; one and sixteen tokens of
+    // the d_model 4096 layer (16 and 56 stages) deal either way.
+    const int grid = gridDim.x, over = pl.units % grid;
+    pl.deal = over > 0 && (int64_t)(grid - over) * pl.steps > (int64_t)kIdleSteps * grid;
+    pl.ctas = pl.deal ? min((pl.units * pl.steps + kMinSteps - 1) / kMinSteps, grid) : min(pl.units, grid);
+    pl.each = pl.deal ? pl.units * pl.steps / pl.ctas : 0;
+    pl.rest = pl.units * pl.steps - pl.each * pl.ctas;
+    if ((int)blockIdx.x >= pl.ctas) {   // nothing to do
         pdl_wait();
         pdl_launch();
         return;
@@ -594,7 +631,6 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) Shared sh;
-    __shared__ int s_most;
     const int tid = threadIdx.x;
     if (tid == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
@@ -602,7 +638,6 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             mbar_init(smem_u32(&sh.empty[s]), kWarps);
         }
         sh.abort = 0;
-        s_most = 0;
         mbar_fence_init();
         prefetch_tmap(&map_a);
         prefetch_tmap(&map_b);
@@ -615,15 +650,7 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         sh.row[i] = (int)(v < 0 ? 0 : (v > p.R_cap ? p.R_cap : v));
     }
     __syncthreads();
-    for (int i = tid; i < p.N; i += kThreads) atomicMax(&s_most, sh.row[i + 1] - sh.row[i]);
-    __syncthreads();
-    const int most = s_most;
-    if (most > 0) {
-        run_tiles<EPI, G, UB>(p, &map_a, &map_b, sh, smem, most);
-    } else {
-        pdl_wait();
-        pdl_launch();
-    }
+    run_tiles<EPI, G, UB>(p, &map_a, &map_b, sh, smem);
     // The other stage's counters: stage 1 clears stage 2's, whose parts come after
     // it, and stage 2 (past its wait) those of the next call's stage 1.
     if (blockIdx.x == 0)
