@@ -810,6 +810,7 @@ static int32_t w4_ffn_impl(const moe_config* cfg, const W4Weights& w, const void
     a.xu = at<float>(ws, W.xu);
     a.hq = at<uint8_t>(ws, W.hq);
     a.hu = at<float>(ws, W.hu);
+    a.h = at<__nv_bfloat16>(ws, L.h);
     a.ye = static_cast<__nv_bfloat16*>(ye);
     a.part = at<float>(ws, W.part);
     a.count = at<int32_t>(ws, L.w4_count);

@@ -46,6 +46,7 @@ struct W4FfnArgs {
     float* xu;             // [R_cap][w4_padded(d) / 64]: their units
     uint8_t* hq;           // [R_cap][w4_padded(d_ff)] x 2 bytes: H
     float* hu;
+    __nv_bfloat16* h;      // [R_cap, d_ff]: H, many rows
     __nv_bfloat16* ye;     // [R_cap, d]
     float* part;           // w4_part_bytes(): sums of tiles that CTAs share
     int32_t* count;        // [2][kW4Counters], zero between calls
@@ -57,6 +58,7 @@ cudaError_t launch_w4_quantize(int64_t mats, int64_t rows, int64_t k, int group,
                                uint16_t* scale, cudaStream_t s);
 cudaError_t launch_w4_dequantize(int64_t mats, int64_t rows, int64_t k, int group, int dtype, const uint8_t* q,
                                  const uint16_t* scale, void* w, cudaStream_t s);
-cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s);
+cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s);      // chooses by the rows per expert
+cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s);   // many rows (w4_tc.cu)
 
 }  // namespace moe

@@ -53,6 +53,8 @@ constexpr int kMinSteps = 2;                     // stages per CTA at least, whe
 constexpr int kIdleSteps = 8;                    // see the plan
 constexpr int kPartFloats = 8 * kRows;          // one fp32 part of a tile
 
+constexpr int kFewRows = 16;                     // rows per expert up to which this kernel is used
+
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
 
 struct GemvParams {
@@ -688,6 +690,7 @@ int w4_gemv_ctas(int sms) { return sms * kCtasPerSm < kW4Counters ? sms * kCtasP
 int64_t w4_part_bytes() { return (int64_t)kW4Counters * 2 * kPartFloats * 4; }
 
 cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
+    if (a.R_cap > (int64_t)kFewRows * a.N) return launch_w4_ffn_tc(a, s);
     int sms = 0;
     cudaError_t err = device_sm_count(&sms);
     if (err != cudaSuccess) return err;
