@@ -14,8 +14,8 @@
 // row's scale, to its fp32 sums in registers -- one fma per output and group.
 // H is rounded to bf16 between the stages, as in the layer on bf16 weights.
 //
-// Roles (320 threads): warp 0 TMA (packed rows; the tokens' rows of x), warp 1 MMA
-// issue and TMEM, warps 2-5 decode, warps 6-9 add up and write out.  TMEM: two
+// Roles (576 threads): warp 0 TMA (packed rows; the tokens' rows of x), warp 1 MMA
+// issue and TMEM, warps 2-9 decode, warps 10-17 add up and write out.  TMEM: two
 // partial accumulators of 128 columns, two A buffers of 64 (128 of K).  SwiGLU
 // puts a feature's W1 row on lane l < 16 and its W3 row on lane l + 16 of the same
 // warp, so the gate and the value meet by a shuffle.
@@ -28,8 +28,9 @@ namespace moe {
 using namespace tc;
 namespace {
 
-constexpr int kThreadsTc = 320;
+constexpr int kThreadsTc = 576;
 constexpr int kTileN = 128;                       // tokens of a tile
+constexpr int kHalfN = kTileN / 2;                // ... of a group of four adding warps
 constexpr int kBoxN = 32;                         // tokens per TMA box
 constexpr int kWStages = 3;                       // packed rows: 256 of K each
 constexpr int kXStages = 4;                       // tokens: 128 of K each
@@ -133,7 +134,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     if (tid == 0) {
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(smem_u32(&sh.wfull[s]), 1);
-            mbar_init(smem_u32(&sh.wempty[s]), 4);
+            mbar_init(smem_u32(&sh.wempty[s]), 8);
         }
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(smem_u32(&sh.xfull[s]), 1);
@@ -143,7 +144,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             mbar_init(smem_u32(&sh.afull[i]), 4);
             mbar_init(smem_u32(&sh.aempty[i]), 1);
             mbar_init(smem_u32(&sh.dfull[i]), 1);
-            mbar_init(smem_u32(&sh.dempty[i]), 4);
+            mbar_init(smem_u32(&sh.dempty[i]), 8);
         }
         mbar_init(smem_u32(&sh.done), 1);
         sh.abort = 0;
@@ -293,24 +294,29 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 drain_bar(smem_u32(&sh.done), 0u, p.limit_ns, p.status);
             }
         }
-    } else if (warp < 6) {
+    } else if (warp < 10) {
         // ---------------- decode: lane = weight row ----------------
+        // two groups of four warps, one for each A buffer: they take blocks in turn
         const int quad = warp & 3;   // TMEM lane quadrant
+        const int a = (warp - 2) >> 2;
         // SwiGLU: lanes 0-15 hold 16 features of W1, lanes 16-31 the same of W3
         const int r = MATS == 2 ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
-        int ws = 0, a = 0;
+        int ws = 0, turn = 0;
         uint32_t wph = 0, aph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            for (int kb = 0; kb < nb && ok; ++kb) {
+            for (int kb = 0; kb < nb && ok; ++kb, turn ^= 1) {
                 if (kb % 2 == 0) ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.wfull[ws]), wph, w));
                 if (!ok) break;
-                const uint8_t* src = smem + ws * kWBytes + r * 128;
+                const bool mine = turn == a;
                 uint4 q[4];
+                if (mine) {
+                    const uint8_t* src = smem + ws * kWBytes + r * 128;
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
-                    q[t] = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + t) ^ (r & 7)) << 4));
-                if (kb % 2 == 1 || kb + 1 == nb) {
+                    for (int t = 0; t < 4; ++t)
+                        q[t] = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + t) ^ (r & 7)) << 4));
+                }
+                if (kb % 2 == 1 || kb + 1 == nb) {   // both groups are done with the stage
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.wempty[ws]));
                     if (++ws == kWStages) {
@@ -318,7 +324,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         wph ^= 1u;
                     }
                 }
+                if (!mine) continue;
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.aempty[a]), aph ^ 1u, w)))) break;
+                aph ^= 1u;
                 tc_fence_after();
                 const uint32_t dst = tmem + kColA + a * 64 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
@@ -339,13 +347,12 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.afull[a]));
-                a ^= 1;
-                if (a == 0) aph ^= 1u;
             }
         }
     } else {
         // ---------------- add up and write out: lane = weight row ----------------
-        const int quad = warp & 3;
+        // two groups of four warps, 64 of the tile's tokens each
+        const int quad = warp & 3, c0 = (warp - 10) / 4 * kHalfN;
         const int f = MATS == 2 ? quad * 16 + (lane & 15) : quad * 32 + lane;   // feature of the tile
         const uint16_t* sc = MATS == 2 && lane >= 16 ? p.sb : p.sa;
         const __nv_bfloat16* bias = MATS == 2 && lane >= 16 ? p.bias_b : p.bias_a;
@@ -358,9 +365,10 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const int feat = t.m0 + f;
             const bool in = feat < p.m_dim;
             const uint16_t* srow = sc + (int64_t)t.e * ng * p.m_dim + (in ? feat : 0);
-            float acc[kTileN];
+            const int n = t.n - c0;   // this group's tokens (may be none)
+            float acc[kHalfN];
 #pragma unroll
-            for (int c = 0; c < kTileN; ++c) acc[c] = 0.f;
+            for (int c = 0; c < kHalfN; ++c) acc[c] = 0.f;
             uint16_t s0 = __ldg(srow), s1 = ng > 1 ? __ldg(srow + p.m_dim) : 0;
             for (int g = 0; g < ng; ++g) {
                 const float s = __uint_as_float((uint32_t)s0 << 16);
@@ -368,15 +376,16 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 s1 = g + 2 < ng ? __ldg(srow + (int64_t)(g + 2) * p.m_dim) : 0;   // two groups ahead
                 if (!(ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.dfull[d]), dph, w)))) break;
                 tc_fence_after();
-                const uint32_t src = tmem + kColD + d * 128 + ((uint32_t)(quad * 32) << 16);
+                const uint32_t src = tmem + kColD + d * 128 + c0 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-                for (int c = 0; c < kTileN / 32; ++c) {
-                    if (32 * c >= t.n) break;
-                    uint32_t v[32];
-                    tmem_ld32(src + 32 * c, v);
-                    tmem_wait_ld();
+                for (int c = 0; c < kHalfN / 16; ++c) {
+                    if (16 * c < n) {
+                        uint32_t v[16];
+                        tmem_ld16(src + 16 * c, v);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[i]), s, acc[32 * c + i]);
+                        for (int i = 0; i < 16; ++i) acc[16 * c + i] = fmaf(__uint_as_float(v[i]), s, acc[16 * c + i]);
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -386,27 +395,26 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             }
             if (!ok) break;
             const float b = in && bias ? __bfloat162float(bias[(int64_t)t.e * p.m_dim + feat]) : 0.f;
-            __nv_bfloat16* dst = p.out + (int64_t)t.row0 * p.m_dim + feat;
+            __nv_bfloat16* dst = p.out + (int64_t)(t.row0 + c0) * p.m_dim + feat;
             if (EPI == W4_SWIGLU) {
                 // lanes < 16 finish the even tokens, their partners the odd ones
 #pragma unroll
-                for (int c = 0; c < kTileN; c += 2) {
-                    if (c >= t.n) break;
+                for (int c = 0; c < kHalfN; c += 2) {
+                    if (c >= n) continue;   // (a break would put acc in local memory)
                     const float mine = lane < 16 ? acc[c] + b : acc[c + 1] + b, send = lane < 16 ? acc[c + 1] + b : acc[c] + b;
                     const float other = __shfl_xor_sync(0xffffffffu, send, 16);
                     const float gate = lane < 16 ? mine : other, up = lane < 16 ? other : mine;
                     const int col = c + (lane >> 4);
-                    if (in && col < t.n)
+                    if (in && col < n)
                         dst[(int64_t)col * p.m_dim] =
                             __float2bfloat16_rn(gate / (1.f + fast_exp2(-gate * kLog2e)) * up);
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < kTileN; ++c) {
-                    if (c >= t.n) break;
+                for (int c = 0; c < kHalfN; ++c) {
                     float o = acc[c] + b;
                     if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
-                    if (in) dst[(int64_t)c * p.m_dim] = __float2bfloat16_rn(o);
+                    if (in && c < n) dst[(int64_t)c * p.m_dim] = __float2bfloat16_rn(o);
                 }
             }
         }
