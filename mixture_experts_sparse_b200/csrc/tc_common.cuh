@@ -58,6 +58,15 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Wa
     }
 }
 
+// wait_bar for hand-overs inside a block's pipeline: the clock is only read after
+// some tries, each of which sleeps for a while or until the phase ends -- reading
+// %globaltimer first would add its latency to every wait that is not met at once.
+__device__ __forceinline__ bool wait_bar_soon(uint32_t bar, uint32_t parity, const Waiter& w) {
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try(bar, parity)) return true;
+    return wait_bar(bar, parity, w);
+}
+
 // Teardown wait: ignores the abort flag, still bounded.
 __device__ __forceinline__ bool drain_bar(uint32_t bar, uint32_t parity, long long limit, int32_t* status) {
     const long long t0 = global_ns();
@@ -247,6 +256,8 @@ bool make_map_bf16_mn_blocks(CUtensorMap* map, const void* base, int64_t rows, i
                              int box_rows, int blocks);
 // host: 2-D bytes [rows, pitch], box = box_rows x 128 bytes, 128-byte swizzle
 bool make_map_u8(CUtensorMap* map, const void* base, int64_t rows, int64_t pitch, int box_rows);
+// host: 2-D 16-bit elements [rows, cols], box = box_rows x box_cols, no swizzle
+bool make_map_u16(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_cols, int box_rows);
 // host: the same over the first `cols` columns of rows `row_stride` elements apart
 bool make_map_bf16_strided(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t row_stride,
                            int box_rows);

@@ -3,8 +3,8 @@
 //   stage 1: H = relu(x W1^T + b1), or silu(x W1^T + b1) * (x W3^T + b3)
 //   stage 2: y = H W2^T + b2              W[o][k] = q[o][k] s[o][k / G]
 //
-// The weights are the A operand: a tile is 128 weight rows by up to 128 tokens, so
-// each word is decoded once for 128 tokens, and a thread that decodes owns one
+// The weights are the A operand: a tile is 128 weight rows by up to 192 tokens, so
+// each word is decoded once for 192 tokens, and a thread that decodes owns one
 // row.  Decoded words are bf16 integers, exact, and go straight into TMEM
 // (tcgen05.st), from where tcgen05.mma reads A: through shared memory the
 // operand would be written and read again beside the tokens' tiles, more than the
@@ -14,11 +14,20 @@
 // row's scale, to its fp32 sums in registers -- one fma per output and group.
 // H is rounded to bf16 between the stages, as in the layer on bf16 weights.
 //
-// Roles (576 threads): warp 0 TMA (packed rows; the tokens' rows of x), warp 1 MMA
-// issue and TMEM, warps 2-9 decode, warps 10-17 add up and write out.  TMEM: two
-// partial accumulators of 128 columns, two A buffers of 64 (128 of K).  SwiGLU
-// puts a feature's W1 row on lane l < 16 and its W3 row on lane l + 16 of the same
-// warp, so the gate and the value meet by a shuffle.
+// Bound: the instructions around the MMAs.  A block of 128 rows x 128 of K is 860
+// warp instructions to decode and, with 192 tokens, about 1100 to add up, for MMAs
+// of 800 cycles; hence the wide tile (all 512 columns of TMEM: two partial
+// accumulators of 192, two A buffers of 64), and 96 sums per adding thread, whose
+// registers setmaxnreg takes from the other warps.  Single-lane branches around
+// TMA, MMA and commit use elect.sync in a warp-uniform loop: with `lane == 0` each
+// such instruction took 45 cycles to issue instead of 9.
+//
+// Roles (five warpgroups): warp 0 TMA of the tokens' rows, 1 MMA issue, 2 TMA of
+// the packed rows and scales (they come from HBM and are asked for further ahead);
+// warps 4-11 decode, in turns, one group per A buffer; warps 12-19 add up and
+// write out, 96 tokens a group.  SwiGLU puts a feature's W1 row on lane l < 16 and
+// its W3 row on lane l + 16 of the same warp, so the gate and the value meet by a
+// shuffle.
 // Every wait is bounded; on expiry the kernel latches MOE_ERR_TIMEOUT, stops
 // issuing, waits (bounded) for its copies and MMAs, frees TMEM and returns.
 #include "tc_common.cuh"
@@ -28,24 +37,32 @@ namespace moe {
 using namespace tc;
 namespace {
 
-constexpr int kThreadsTc = 576;
-constexpr int kTileN = 128;                       // tokens of a tile
-constexpr int kHalfN = kTileN / 2;                // ... of a group of four adding warps
+constexpr int kThreadsTc = 640;
+constexpr int kTileN = 192;                       // tokens of a tile
+constexpr int kPartN = kTileN / 2;                // ... of a group of adding warps
 constexpr int kBoxN = 32;                         // tokens per TMA box
-constexpr int kWStages = 3;                       // packed rows: 256 of K each
-constexpr int kXStages = 4;                       // tokens: 128 of K each
+constexpr int kWStages = 4;                       // packed rows and scales: 256 of K each
+constexpr int kXStages = 3;                       // tokens: 128 of K each
 constexpr int kWBytes = 128 * 128;
 constexpr int kXSub = kTileN * 128;               // 64 of K
 constexpr int kXBytes = 2 * kXSub;
-constexpr int kSmemTc = kWStages * kWBytes + kXStages * kXBytes + 1024;
-constexpr uint32_t kColD = 0, kColA = 256;        // TMEM columns
+constexpr int kSBytes = 2048;                     // scales of a stage: 2 boxes x 256 / G groups x 64 rows
+constexpr int kSmemTc = kWStages * (kWBytes + kSBytes) + kXStages * kXBytes + 1024;
+constexpr uint32_t kColD = 0, kColA = 2 * kTileN; // TMEM columns
+// Registers per thread: the launch's 640 x 96 are dealt out anew, 40 + 2 x 72 +
+// 2 x 144 = 472 <= 5 x 96 per warpgroup lane.
+constexpr int kRegsControl = 40, kRegsDecode = 72, kRegsAdd = 144;
+static_assert(kRegsControl + 2 * kRegsDecode + 2 * kRegsAdd <= 5 * 96, "register pool");
+template <int R>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
 
 struct TcParams {
     const int32_t* offsets; int N; int64_t R_cap;
     int m_dim, k_dim;
-    const uint16_t* sa; const uint16_t* sb;
     const __nv_bfloat16* bias_a; const __nv_bfloat16* bias_b;
     __nv_bfloat16* out;           // [R, m_dim]
     int32_t* status;
@@ -73,6 +90,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Weights 2 p and 2 p + 1 of a word's eight as a bf16 pair of integers: 128 + (q + 8)
 // is exact in bf16 (0x4300 is 128, whose last place is 1), and so is the difference.
 __device__ __forceinline__ uint32_t decode_pair(uint32_t w, int p) {
@@ -85,8 +109,12 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w, int p) {
 }
 
 struct SharedTc {
-    uint64_t wfull[kWStages], wempty[kWStages], xfull[kXStages], xempty[kXStages];
-    uint64_t afull[2], aempty[2], dfull[2], dempty[2], done;
+    uint64_t wfull[kWStages], wempty[kWStages], sempty[kWStages];   // wfull: rows and scales
+    uint64_t xfull[kXStages], xempty[kXStages];
+    uint64_t afull[2];              // a block's weights are in TMEM
+    uint64_t mdone[2];              // its MMAs are done: A is free, (G = 128) its sums are there
+    uint64_t dfull[2], dempty[2];   // partial accumulators; dfull: G < 128
+    uint64_t done;
     uint32_t tmem;
     int abort, live;
     int row[129], exp[128], first[129];
@@ -96,7 +124,7 @@ struct Tile {
     int e, m0, row0, n;
 };
 
-// rows of an expert in equal chunks of at most 128, a multiple of 16
+// rows of an expert in equal chunks of at most 192, a multiple of 16
 __device__ __forceinline__ int chunk_rows(int n) {
     const int chunks = (n + kTileN - 1) / kTileN;
     return ((n + chunks - 1) / chunks + 15) / 16 * 16;
@@ -122,6 +150,7 @@ __device__ __forceinline__ Tile tile_of(const SharedTc& sh, int u, int feats) {
 template <int EPI, int G>
 __global__ void __launch_bounds__(kThreadsTc, 1)
 w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+             const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
              const __grid_constant__ CUtensorMap map_x, const TcParams p) {
     constexpr int MATS = EPI == W4_SWIGLU ? 2 : 1;
     constexpr int FEATS = 128 / MATS;
@@ -129,12 +158,14 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* smem_x = smem + kWStages * kWBytes;
+    uint8_t* smem_s = smem_x + kXStages * kXBytes;
     __shared__ __align__(8) SharedTc sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(smem_u32(&sh.wfull[s]), 1);
             mbar_init(smem_u32(&sh.wempty[s]), 8);
+            mbar_init(smem_u32(&sh.sempty[s]), 8);
         }
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(smem_u32(&sh.xfull[s]), 1);
@@ -142,7 +173,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.afull[i]), 4);
-            mbar_init(smem_u32(&sh.aempty[i]), 1);
+            mbar_init(smem_u32(&sh.mdone[i]), 1);
             mbar_init(smem_u32(&sh.dfull[i]), 1);
             mbar_init(smem_u32(&sh.dempty[i]), 8);
         }
@@ -161,7 +192,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     }
     __syncthreads();
     const int tiles = (p.m_dim + FEATS - 1) / FEATS;
-    if (warp == 2) {   // live experts and their first units: four experts a lane, a scan over the lanes
+    if (warp == 3) {   // live experts and their first units: four experts a lane, a scan over the lanes
         int n[4], live = 0, units = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -201,40 +232,29 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const int nb = (p.k_dim + kW4Block - 1) / kW4Block;   // blocks of 128
     const Waiter w{&sh.abort, p.status, p.limit_ns};
 
-    if (warp == 0) {
-        // ---------------- TMA ----------------
-        if (lane == 0) {
-            int ws = 0, xs = 0;
-            uint32_t wph = 0, xph = 0, wused = 0, xused = 0;
+    if (warp < 4) {
+        regs_dec<kRegsControl>();
+        if (warp == 0) {
+            // ---------------- TMA: the tokens' rows ----------------
+            int xs = 0;
+            uint32_t xph = 0, xused = 0;
             bool ok = true;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const Tile t = tile_of(sh, u, FEATS);
-                const int row = t.e * p.m_dim + t.m0;
-                const bool second = MATS == 2 || t.m0 + 64 < p.m_dim;   // the upper 64 rows hold something
                 const int boxes = (t.n + kBoxN - 1) / kBoxN;
                 for (int kb = 0; kb < nb; ++kb) {
-                    if (kb % 2 == 0) {
-                        if (!(ok = wait_bar(smem_u32(&sh.wempty[ws]), wph ^ 1u, w))) break;
-                        const uint32_t fb = smem_u32(&sh.wfull[ws]), dst = smem_u32(smem + ws * kWBytes);
-                        mbar_expect_tx(fb, second ? kWBytes : kWBytes / 2);
-                        tma_load_2d(dst, &map_a, fb, kb * kW4BlockBytes, row);
-                        if (second)
-                            tma_load_2d(dst + kWBytes / 2, MATS == 2 ? &map_b : &map_a, fb, kb * kW4BlockBytes,
-                                        MATS == 2 ? row : row + 64);
-                        wused |= 1u << ws;
-                        if (++ws == kWStages) {
-                            ws = 0;
-                            wph ^= 1u;
-                        }
-                    }
-                    if (!(ok = wait_bar(smem_u32(&sh.xempty[xs]), xph ^ 1u, w))) break;
-                    const uint32_t fb = smem_u32(&sh.xfull[xs]), dst = smem_u32(smem_x + xs * kXBytes);
+                    ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.xempty[xs]), xph ^ 1u, w));
+                    if (!ok) break;
+                    const uint32_t fb = smem_u32(&sh.xfull[xs]), dst = smem_u32(smem_x) + xs * kXBytes;
                     const int halves = kb * kW4Block + 64 < p.k_dim ? 2 : 1;
-                    mbar_expect_tx(fb, halves * boxes * kBoxN * 128);
-                    for (int h = 0; h < halves; ++h)
-                        for (int b = 0; b < boxes; ++b)
-                            tma_load_2d(dst + h * kXSub + b * kBoxN * 128, &map_x, fb, kb * kW4Block + h * 64,
-                                        t.row0 + b * kBoxN);
+                    if (elect_one()) {
+                        mbar_expect_tx(fb, halves * boxes * kBoxN * 128);
+                        for (int h = 0; h < halves; ++h)
+                            for (int b = 0; b < boxes; ++b)
+                                tma_load_2d(dst + h * kXSub + b * kBoxN * 128, &map_x, fb, kb * kW4Block + h * 64,
+                                            t.row0 + b * kBoxN);
+                    }
+                    __syncwarp();
                     xused |= 1u << xs;
                     if (++xs == kXStages) {
                         xs = 0;
@@ -242,45 +262,86 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     }
                 }
             }
-            // every load has landed before the CTA retires (normally long consumed)
-            for (int s = 0; s < kWStages; ++s)
-                if (wused >> s & 1u) drain_bar(smem_u32(&sh.wfull[s]), s < ws ? wph : wph ^ 1u, p.limit_ns, p.status);
+            // every load has landed before the CTA retires
             for (int s = 0; s < kXStages; ++s)
                 if (xused >> s & 1u) drain_bar(smem_u32(&sh.xfull[s]), s < xs ? xph : xph ^ 1u, p.limit_ns, p.status);
-        }
-    } else if (warp == 1) {
-        // ---------------- MMA ----------------
-        if (lane == 0) {
+        } else if (warp == 2) {
+            // ---------------- TMA: packed rows and scales ----------------
+            int ws = 0;
+            uint32_t wph = 0, wused = 0;
+            bool ok = true;
+            const int ng = (p.k_dim + G - 1) / G;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const Tile t = tile_of(sh, u, FEATS);
+                const int row = t.e * p.m_dim + t.m0;
+                const bool second = MATS == 2 || t.m0 + 64 < p.m_dim;   // the upper 64 rows hold something
+                for (int kb = 0; kb < nb; kb += 2) {
+                    ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wempty[ws]), wph ^ 1u, w) &&
+                                                     wait_bar_soon(smem_u32(&sh.sempty[ws]), wph ^ 1u, w));
+                    if (!ok) break;
+                    constexpr int SB = 2 * PER * 128;   // one box of scales
+                    const uint32_t fb = smem_u32(&sh.wfull[ws]), dst = smem_u32(smem) + ws * kWBytes;
+                    const uint32_t sdst = smem_u32(smem_s) + ws * kSBytes;
+                    if (elect_one()) {
+                        mbar_expect_tx(fb, (second ? 2 : 1) * (kWBytes / 2 + SB));
+                        tma_load_2d(dst, &map_a, fb, kb * kW4BlockBytes, row);
+                        tma_load_2d(sdst, &map_sa, fb, t.m0, t.e * ng + kb * PER);
+                        if (second) {
+                            tma_load_2d(dst + kWBytes / 2, MATS == 2 ? &map_b : &map_a, fb, kb * kW4BlockBytes,
+                                        MATS == 2 ? row : row + 64);
+                            tma_load_2d(sdst + SB, MATS == 2 ? &map_sb : &map_sa, fb, MATS == 2 ? t.m0 : t.m0 + 64,
+                                        t.e * ng + kb * PER);
+                        }
+                    }
+                    __syncwarp();
+                    wused |= 1u << ws;
+                    if (++ws == kWStages) {
+                        ws = 0;
+                        wph ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < kWStages; ++s)
+                if (wused >> s & 1u) drain_bar(smem_u32(&sh.wfull[s]), s < ws ? wph : wph ^ 1u, p.limit_ns, p.status);
+        } else if (warp == 1) {
+            // ---------------- MMA ----------------
             int xs = 0, a = 0, d = 0;
             uint32_t xph = 0, aph = 0, dph = 0;
             bool ok = true, issued = false;
+            const uint64_t bd0 = umma_desc(smem_u32(smem_x));
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const Tile t = tile_of(sh, u, FEATS);
                 const uint32_t idesc = idesc_bf16_f32(128, (t.n + 15) / 16 * 16);
                 for (int kb = 0; kb < nb && ok; ++kb) {
-                    ok = wait_bar(smem_u32(&sh.xfull[xs]), xph, w) && wait_bar(smem_u32(&sh.afull[a]), aph, w);
+                    ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.afull[a]), aph, w) &&
+                                                     wait_bar_soon(smem_u32(&sh.xfull[xs]), xph, w));
                     if (!ok) break;
-                    const uint64_t bd = umma_desc(smem_u32(smem_x + xs * kXBytes));
+                    const uint64_t bd = bd0 + (uint64_t)(xs * (kXBytes >> 4));
                     const uint32_t ad = tmem + kColA + a * 64;
                     const int nk = min(8, (p.k_dim - kb * kW4Block) / 16);   // K is a multiple of 16
 #pragma unroll
                     for (int gi = 0; gi < PER; ++gi) {
                         if (gi * (8 / PER) >= nk) break;
-                        if (!(ok = wait_bar(smem_u32(&sh.dempty[d]), dph ^ 1u, w))) break;
+                        if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.dempty[d]), dph ^ 1u, w)))) break;
                         tc_fence_after();
                         issued = true;
+                        const uint32_t dd = tmem + kColD + d * kTileN;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int kk = gi * (8 / PER); kk < (gi + 1) * (8 / PER); ++kk)
-                            if (kk < nk)
-                                umma_ts(tmem + kColD + d * 128, ad + 8 * kk, bd + (uint64_t)((kk / 4 * kXSub) >> 4) + 2 * (kk % 4),
-                                        idesc, kk > gi * (8 / PER));
-                        umma_commit(smem_u32(&sh.dfull[d]));
+                            for (int kk = gi * (8 / PER); kk < (gi + 1) * (8 / PER); ++kk)
+                                if (kk < nk)
+                                    umma_ts(dd, ad + 8 * kk, bd + (uint64_t)((kk / 4 * kXSub) >> 4) + 2 * (kk % 4), idesc,
+                                            kk > gi * (8 / PER));
+                            if (PER > 1) umma_commit(smem_u32(&sh.dfull[d]));
+                            if (gi == PER - 1 || (gi + 1) * (8 / PER) >= nk) {
+                                umma_commit(smem_u32(&sh.mdone[a]));
+                                umma_commit(smem_u32(&sh.xempty[xs]));
+                            }
+                        }
+                        __syncwarp();
                         d ^= 1;
                         if (d == 0) dph ^= 1u;
                     }
-                    if (!ok) break;
-                    umma_commit(smem_u32(&sh.aempty[a]));
-                    umma_commit(smem_u32(&sh.xempty[xs]));
                     a ^= 1;
                     if (a == 0) aph ^= 1u;
                     if (++xs == kXStages) {
@@ -290,15 +351,17 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
             }
             if (issued) {   // every MMA has completed before TMEM is freed
-                umma_commit(smem_u32(&sh.done));
+                if (elect_one()) umma_commit(smem_u32(&sh.done));
+                __syncwarp();
                 drain_bar(smem_u32(&sh.done), 0u, p.limit_ns, p.status);
             }
         }
-    } else if (warp < 10) {
+    } else if (warp < 12) {
         // ---------------- decode: lane = weight row ----------------
         // two groups of four warps, one for each A buffer: they take blocks in turn
+        regs_dec<kRegsDecode>();
         const int quad = warp & 3;   // TMEM lane quadrant
-        const int a = (warp - 2) >> 2;
+        const int a = (warp - 4) >> 2;
         // SwiGLU: lanes 0-15 hold 16 features of W1, lanes 16-31 the same of W3
         const int r = MATS == 2 ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
         int ws = 0, turn = 0;
@@ -306,7 +369,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             for (int kb = 0; kb < nb && ok; ++kb, turn ^= 1) {
-                if (kb % 2 == 0) ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.wfull[ws]), wph, w));
+                if (kb % 2 == 0) ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w));
                 if (!ok) break;
                 const bool mine = turn == a;
                 uint4 q[4];
@@ -316,7 +379,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     for (int t = 0; t < 4; ++t)
                         q[t] = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + t) ^ (r & 7)) << 4));
                 }
-                if (kb % 2 == 1 || kb + 1 == nb) {   // both groups are done with the stage
+                if (kb % 2 == 1 || kb + 1 == nb) {   // this warp is done with the stage
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sh.wempty[ws]));
                     if (++ws == kWStages) {
@@ -325,7 +388,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     }
                 }
                 if (!mine) continue;
-                if (!(ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.aempty[a]), aph ^ 1u, w)))) break;
+                if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.mdone[a]), aph ^ 1u, w)))) break;
                 aph ^= 1u;
                 tc_fence_after();
                 const uint32_t dst = tmem + kColA + a * 64 + ((uint32_t)(quad * 32) << 16);
@@ -351,40 +414,50 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
     } else {
         // ---------------- add up and write out: lane = weight row ----------------
-        // two groups of four warps, 64 of the tile's tokens each
-        const int quad = warp & 3, c0 = (warp - 10) / 4 * kHalfN;
+        // two groups of four warps, 96 of the tile's tokens each
+        regs_inc<kRegsAdd>();
+        const int quad = warp & 3, c0 = (warp - 12) / 4 * kPartN;
         const int f = MATS == 2 ? quad * 16 + (lane & 15) : quad * 32 + lane;   // feature of the tile
-        const uint16_t* sc = MATS == 2 && lane >= 16 ? p.sb : p.sa;
+        // its scales in a stage: box, then 64 features a group
+        const int soff = (MATS == 2 ? (lane >> 4) * (2 * PER * 64) + f : f / 64 * (2 * PER * 64) + f % 64) * 2;
         const __nv_bfloat16* bias = MATS == 2 && lane >= 16 ? p.bias_b : p.bias_a;
         const int ng = (p.k_dim + G - 1) / G;
-        int d = 0;
-        uint32_t dph = 0;
+        int d = 0, ws = 0;
+        uint32_t dph = 0, wph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const Tile t = tile_of(sh, u, FEATS);
             const int feat = t.m0 + f;
             const bool in = feat < p.m_dim;
-            const uint16_t* srow = sc + (int64_t)t.e * ng * p.m_dim + (in ? feat : 0);
             const int n = t.n - c0;   // this group's tokens (may be none)
-            float acc[kHalfN];
+            float acc[kPartN];
 #pragma unroll
-            for (int c = 0; c < kHalfN; ++c) acc[c] = 0.f;
-            uint16_t s0 = __ldg(srow), s1 = ng > 1 ? __ldg(srow + p.m_dim) : 0;
+            for (int c = 0; c < kPartN; ++c) acc[c] = 0.f;
             for (int g = 0; g < ng; ++g) {
-                const float s = __uint_as_float((uint32_t)s0 << 16);
-                s0 = s1;
-                s1 = g + 2 < ng ? __ldg(srow + (int64_t)(g + 2) * p.m_dim) : 0;   // two groups ahead
-                if (!(ok = __all_sync(0xffffffffu, wait_bar(smem_u32(&sh.dfull[d]), dph, w)))) break;
+                const int gs = g % (2 * PER);   // group of the stage
+                if (gs == 0 && !(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w)))) break;
+                const float s = __uint_as_float(
+                    (uint32_t)*reinterpret_cast<const uint16_t*>(smem_s + ws * kSBytes + gs * 128 + soff) << 16);
+                if (gs == 2 * PER - 1 || g + 1 == ng) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.sempty[ws]));
+                    if (++ws == kWStages) {
+                        ws = 0;
+                        wph ^= 1u;
+                    }
+                }
+                ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(PER > 1 ? &sh.dfull[d] : &sh.mdone[d]), dph, w));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t src = tmem + kColD + d * 128 + c0 + ((uint32_t)(quad * 32) << 16);
+                const uint32_t src = tmem + kColD + d * kTileN + c0 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-                for (int c = 0; c < kHalfN / 16; ++c) {
-                    if (16 * c < n) {
-                        uint32_t v[16];
-                        tmem_ld16(src + 16 * c, v);
+                for (int c = 0; c < kPartN / 32; ++c) {
+                    if (32 * c < n) {
+                        uint32_t v[32];
+                        tmem_ld32(src + 32 * c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[16 * c + i] = fmaf(__uint_as_float(v[i]), s, acc[16 * c + i]);
+                        for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[i]), s, acc[32 * c + i]);
                     }
                 }
                 tc_fence_before();
@@ -399,7 +472,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             if (EPI == W4_SWIGLU) {
                 // lanes < 16 finish the even tokens, their partners the odd ones
 #pragma unroll
-                for (int c = 0; c < kHalfN; c += 2) {
+                for (int c = 0; c < kPartN; c += 2) {
                     if (c >= n) continue;   // (a break would put acc in local memory)
                     const float mine = lane < 16 ? acc[c] + b : acc[c + 1] + b, send = lane < 16 ? acc[c + 1] + b : acc[c] + b;
                     const float other = __shfl_xor_sync(0xffffffffu, send, 16);
@@ -411,7 +484,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < kHalfN; ++c) {
+                for (int c = 0; c < kPartN; ++c) {
                     float o = acc[c] + b;
                     if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
                     if (in && c < n) dst[(int64_t)c * p.m_dim] = __float2bfloat16_rn(o);
@@ -426,22 +499,31 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 }
 
 template <int EPI, int G>
-cudaError_t run_tc_g(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& x, const TcParams& p, int sms,
-                     cudaStream_t s) {
+cudaError_t run_tc_g(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& sa, const CUtensorMap& sb,
+                     const CUtensorMap& x, const TcParams& p, int sms, cudaStream_t s) {
     auto kern = w4_tc_kernel<EPI, G>;
     cudaError_t err = once_per_device(reinterpret_cast<const void*>(kern), [](const void* k) {
         return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTc);
     });
     if (err != cudaSuccess) return err;
-    return launch_k(kern, dim3((unsigned)sms), dim3(kThreadsTc), kSmemTc, s, 1, a, b, x, p);
+    return launch_k(kern, dim3((unsigned)sms), dim3(kThreadsTc), kSmemTc, s, 1, a, b, sa, sb, x, p);
 }
 
+// one matrix of a stage: its packed rows and its scales
+struct Maps {
+    CUtensorMap q, s;
+    bool make(const W4Mat& w, int N, int rows, int k, int group) {
+        return make_map_u8(&q, w.q, (int64_t)N * rows, w4_row_bytes(k), 64) &&
+               make_map_u16(&s, w.s, (int64_t)N * ((k + group - 1) / group), rows, 64, 256 / group);
+    }
+};
+
 template <int EPI>
-cudaError_t run_tc(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& x, const TcParams& p, int group, int sms,
+cudaError_t run_tc(const Maps& a, const Maps& b, const CUtensorMap& x, const TcParams& p, int group, int sms,
                    cudaStream_t s) {
-    if (group == 32) return run_tc_g<EPI, 32>(a, b, x, p, sms, s);
-    if (group == 64) return run_tc_g<EPI, 64>(a, b, x, p, sms, s);
-    return run_tc_g<EPI, 128>(a, b, x, p, sms, s);
+    if (group == 32) return run_tc_g<EPI, 32>(a.q, b.q, a.s, b.s, x, p, sms, s);
+    if (group == 64) return run_tc_g<EPI, 64>(a.q, b.q, a.s, b.s, x, p, sms, s);
+    return run_tc_g<EPI, 128>(a.q, b.q, a.s, b.s, x, p, sms, s);
 }
 
 }  // namespace
@@ -450,14 +532,13 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     int sms = 0;
     cudaError_t err = device_sm_count(&sms);
     if (err != cudaSuccess) return err;
-    CUtensorMap m1, m3, m2, mx, mh;
-    if (!make_map_u8(&m1, a.w1.q, (int64_t)a.N * a.d_ff, w4_row_bytes(a.d), 64) ||
-        !make_map_u8(&m2, a.w2.q, (int64_t)a.N * a.d, w4_row_bytes(a.d_ff), 64) ||
+    Maps m1, m3, m2;
+    CUtensorMap mx, mh;
+    if (!m1.make(a.w1, a.N, a.d_ff, a.d, a.group) || !m2.make(a.w2, a.N, a.d, a.d_ff, a.group) ||
         !make_map_bf16(&mx, a.xe, a.R_cap, a.d, kBoxN) || !make_map_bf16(&mh, a.h, a.R_cap, a.d_ff, kBoxN))
         return cudaErrorInvalidValue;
     m3 = m1;
-    if (a.act == MOE_SWIGLU && !make_map_u8(&m3, a.w3.q, (int64_t)a.N * a.d_ff, w4_row_bytes(a.d), 64))
-        return cudaErrorInvalidValue;
+    if (a.act == MOE_SWIGLU && !m3.make(a.w3, a.N, a.d_ff, a.d, a.group)) return cudaErrorInvalidValue;
     TcParams p{};
     p.offsets = a.offsets;
     p.N = a.N;
@@ -466,8 +547,6 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     p.limit_ns = kWaitLimitNs;
     p.m_dim = a.d_ff;
     p.k_dim = a.d;
-    p.sa = a.w1.s;
-    p.sb = a.w3.s;
     p.bias_a = a.b1;
     p.bias_b = a.b3;
     p.out = a.h;
@@ -476,7 +555,6 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     if (err != cudaSuccess) return err;
     p.m_dim = a.d;
     p.k_dim = a.d_ff;
-    p.sa = a.w2.s;
     p.bias_a = a.b2;
     p.bias_b = nullptr;
     p.out = a.ye;
