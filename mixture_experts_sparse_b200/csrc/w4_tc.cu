@@ -37,9 +37,10 @@ namespace moe {
 using namespace tc;
 namespace {
 
-constexpr int kThreadsTc = 640;
+constexpr int kAddGroups = 2;                     // warpgroups that add up
+constexpr int kThreadsTc = 128 * (3 + kAddGroups);
 constexpr int kTileN = 192;                       // tokens of a tile
-constexpr int kPartN = kTileN / 2;                // ... of a group of adding warps
+constexpr int kPartN = kTileN / kAddGroups;       // ... of a group of adding warps
 constexpr int kBoxN = 32;                         // tokens per TMA box
 constexpr int kWStages = 4;                       // packed rows and scales: 256 of K each
 constexpr int kXStages = 3;                       // tokens: 128 of K each
@@ -51,8 +52,8 @@ constexpr int kSmemTc = kWStages * (kWBytes + kSBytes) + kXStages * kXBytes + 10
 constexpr uint32_t kColD = 0, kColA = 2 * kTileN; // TMEM columns
 // Registers per thread: the launch's 640 x 96 are dealt out anew, 40 + 2 x 72 +
 // 2 x 144 = 472 <= 5 x 96 per warpgroup lane.
-constexpr int kRegsControl = 40, kRegsDecode = 72, kRegsAdd = 144;
-static_assert(kRegsControl + 2 * kRegsDecode + 2 * kRegsAdd <= 5 * 96, "register pool");
+constexpr int kRegsLaunch = 96, kRegsControl = 32, kRegsDecode = 64, kRegsAdd = 160;
+static_assert(kRegsControl + 2 * kRegsDecode + kAddGroups * kRegsAdd <= (3 + kAddGroups) * kRegsLaunch, "register pool");
 template <int R>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -89,6 +90,21 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// two fp32 fused multiply-adds in one instruction
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
 
 // one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
@@ -165,7 +181,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(smem_u32(&sh.wfull[s]), 1);
             mbar_init(smem_u32(&sh.wempty[s]), 8);
-            mbar_init(smem_u32(&sh.sempty[s]), 8);
+            mbar_init(smem_u32(&sh.sempty[s]), 4 * kAddGroups);
         }
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(smem_u32(&sh.xfull[s]), 1);
@@ -175,7 +191,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             mbar_init(smem_u32(&sh.afull[i]), 4);
             mbar_init(smem_u32(&sh.mdone[i]), 1);
             mbar_init(smem_u32(&sh.dfull[i]), 1);
-            mbar_init(smem_u32(&sh.dempty[i]), 8);
+            mbar_init(smem_u32(&sh.dempty[i]), 4 * kAddGroups);
         }
         mbar_init(smem_u32(&sh.done), 1);
         sh.abort = 0;
@@ -430,9 +446,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const int feat = t.m0 + f;
             const bool in = feat < p.m_dim;
             const int n = t.n - c0;   // this group's tokens (may be none)
-            float acc[kPartN];
+            uint64_t acc2[kPartN / 2];   // pairs of fp32 sums (fma.rn.f32x2)
 #pragma unroll
-            for (int c = 0; c < kPartN; ++c) acc[c] = 0.f;
+            for (int c = 0; c < kPartN / 2; ++c) acc2[c] = 0;
             for (int g = 0; g < ng; ++g) {
                 const int gs = g % (2 * PER);   // group of the stage
                 if (gs == 0 && !(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w)))) break;
@@ -450,6 +466,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t src = tmem + kColD + d * kTileN + c0 + ((uint32_t)(quad * 32) << 16);
+                const uint64_t s2 = pack_f32x2(s, s);
 #pragma unroll
                 for (int c = 0; c < kPartN / 32; ++c) {
                     if (32 * c < n) {
@@ -457,7 +474,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         tmem_ld32(src + 32 * c, v);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[32 * c + i] = fmaf(__uint_as_float(v[i]), s, acc[32 * c + i]);
+                        for (int i = 0; i < 16; ++i)
+                            acc2[16 * c + i] = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2,
+                                                         acc2[16 * c + i]);
                     }
                 }
                 tc_fence_before();
@@ -467,6 +486,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 if (d == 0) dph ^= 1u;
             }
             if (!ok) break;
+            float acc[kPartN];
+#pragma unroll
+            for (int c = 0; c < kPartN / 2; ++c) unpack_f32x2(acc2[c], acc[2 * c], acc[2 * c + 1]);
             const float b = in && bias ? __bfloat162float(bias[(int64_t)t.e * p.m_dim + feat]) : 0.f;
             __nv_bfloat16* dst = p.out + (int64_t)(t.row0 + c0) * p.m_dim + feat;
             if (EPI == W4_SWIGLU) {
