@@ -78,16 +78,10 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
-        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
-        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
-        : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -188,7 +182,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             mbar_init(smem_u32(&sh.xempty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.afull[i]), 4);
+            mbar_init(smem_u32(&sh.afull[i]), 8);
             mbar_init(smem_u32(&sh.mdone[i]), 1);
             mbar_init(smem_u32(&sh.dfull[i]), 1);
             mbar_init(smem_u32(&sh.dempty[i]), 4 * kAddGroups);
@@ -374,26 +368,32 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
     } else if (warp < 12) {
         // ---------------- decode: lane = weight row ----------------
-        // two groups of four warps, one for each A buffer: they take blocks in turn
+        // two groups of four warps, half of every block each: the words t = 2 h, 2 h + 1,
+        // columns 16 j + 8 h .. + 7.  They decode into registers before they wait for
+        // the A buffer, so only the stores are between one MMA and the next but one.
         regs_dec<kRegsDecode>();
         const int quad = warp & 3;   // TMEM lane quadrant
-        const int a = (warp - 4) >> 2;
+        const int h = (warp - 4) >> 2;
         // SwiGLU: lanes 0-15 hold 16 features of W1, lanes 16-31 the same of W3
         const int r = MATS == 2 ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
-        int ws = 0, turn = 0;
+        int ws = 0, a = 0;
         uint32_t wph = 0, aph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            for (int kb = 0; kb < nb && ok; ++kb, turn ^= 1) {
+            for (int kb = 0; kb < nb && ok; ++kb) {
                 if (kb % 2 == 0) ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w));
                 if (!ok) break;
-                const bool mine = turn == a;
-                uint4 q[4];
-                if (mine) {
-                    const uint8_t* src = smem + ws * kWBytes + r * 128;
+                const uint8_t* src = smem + ws * kWBytes + r * 128;
+                uint32_t v[32];
 #pragma unroll
-                    for (int t = 0; t < 4; ++t)
-                        q[t] = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + t) ^ (r & 7)) << 4));
+                for (int t = 0; t < 2; ++t) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + 2 * h + t) ^ (r & 7)) << 4));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t word = j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[8 * j + 4 * t + i] = decode_pair(word, i);
+                    }
                 }
                 if (kb % 2 == 1 || kb + 1 == nb) {   // this warp is done with the stage
                     __syncwarp();
@@ -403,29 +403,17 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         wph ^= 1u;
                     }
                 }
-                if (!mine) continue;
                 if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.mdone[a]), aph ^ 1u, w)))) break;
-                aph ^= 1u;
                 tc_fence_after();
-                const uint32_t dst = tmem + kColA + a * 64 + ((uint32_t)(quad * 32) << 16);
+                const uint32_t dst = tmem + kColA + a * 64 + 8 * h + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {   // columns 32 half .. : words j = 2 half, 2 half + 1
-                    uint32_t v[32];
-#pragma unroll
-                    for (int jj = 0; jj < 2; ++jj)
-#pragma unroll
-                        for (int t = 0; t < 4; ++t) {
-                            const int j = 2 * half + jj;
-                            const uint32_t word = j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) v[16 * jj + 4 * t + i] = decode_pair(word, i);
-                        }
-                    tmem_st32(dst + 32 * half, v);
-                }
+                for (int j = 0; j < 4; ++j) tmem_st8(dst + 16 * j, v + 8 * j);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.afull[a]));
+                a ^= 1;
+                if (a == 0) aph ^= 1u;
             }
         }
     } else {
@@ -467,21 +455,25 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 tc_fence_after();
                 const uint32_t src = tmem + kColD + d * kTileN + c0 + ((uint32_t)(quad * 32) << 16);
                 const uint64_t s2 = pack_f32x2(s, s);
+                auto release = [&]() {   // this warp's last read of the buffer
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.dempty[d]));
+                };
+                if (n <= 0) release();
 #pragma unroll
                 for (int c = 0; c < kPartN / 32; ++c) {
                     if (32 * c < n) {
                         uint32_t v[32];
                         tmem_ld32(src + 32 * c, v);
                         tmem_wait_ld();
+                        if (32 * (c + 1) >= n || c + 1 == kPartN / 32) release();
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             acc2[16 * c + i] = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2,
                                                          acc2[16 * c + i]);
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.dempty[d]));
                 d ^= 1;
                 if (d == 0) dph ^= 1u;
             }
@@ -493,23 +485,29 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             __nv_bfloat16* dst = p.out + (int64_t)(t.row0 + c0) * p.m_dim + feat;
             if (EPI == W4_SWIGLU) {
                 // lanes < 16 finish the even tokens, their partners the odd ones
+                const bool low = lane < 16;
+                if (!low) dst += p.m_dim;
 #pragma unroll
                 for (int c = 0; c < kPartN; c += 2) {
-                    if (c >= n) continue;   // (a break would put acc in local memory)
-                    const float mine = lane < 16 ? acc[c] + b : acc[c + 1] + b, send = lane < 16 ? acc[c + 1] + b : acc[c] + b;
-                    const float other = __shfl_xor_sync(0xffffffffu, send, 16);
-                    const float gate = lane < 16 ? mine : other, up = lane < 16 ? other : mine;
-                    const int col = c + (lane >> 4);
-                    if (in && col < n)
-                        dst[(int64_t)col * p.m_dim] =
-                            __float2bfloat16_rn(gate / (1.f + fast_exp2(-gate * kLog2e)) * up);
+                    if (c < n) {   // (a break would put acc in local memory)
+                        const float mine = (low ? acc[c] : acc[c + 1]) + b, send = (low ? acc[c + 1] : acc[c]) + b;
+                        const float other = __shfl_xor_sync(0xffffffffu, send, 16);
+                        const float gate = low ? mine : other, up = low ? other : mine;
+                        // e^-z -> inf for very negative z: the fast division gives the limit 0
+                        const float o = __fdividef(gate, 1.f + fast_exp2(-gate * kLog2e)) * up;
+                        if (in && (low || c + 1 < n)) *dst = __float2bfloat16_rn(o);
+                        dst += 2 * p.m_dim;
+                    }
                 }
             } else {
 #pragma unroll
                 for (int c = 0; c < kPartN; ++c) {
-                    float o = acc[c] + b;
-                    if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
-                    if (in && c < n) dst[(int64_t)c * p.m_dim] = __float2bfloat16_rn(o);
+                    if (c < n) {
+                        float o = acc[c] + b;
+                        if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
+                        if (in) *dst = __float2bfloat16_rn(o);
+                        dst += p.m_dim;
+                    }
                 }
             }
         }
