@@ -714,7 +714,7 @@ static bool w4_group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
 // the layer workspace, then the rows of x and H as integers with their units, then
 // the sums of tiles that CTAs share
 struct W4Layout {
-    size_t xq, xu, hq, hu, part, total;
+    size_t xq, xu, hq, hu, part, wexp, top, total;
 };
 static W4Layout w4_layout(const moe_config& c, const Layout& L) {
     W4Layout w{};
@@ -731,6 +731,8 @@ static W4Layout w4_layout(const moe_config& c, const Layout& L) {
     w.hq = take(2 * R * f);
     w.hu = take(4 * R * (f / kW4ActBlock));
     w.part = take((size_t)w4_part_bytes());
+    w.wexp = take((size_t)c.n_experts * (2 * (size_t)c.d_ff + (size_t)c.d_model));
+    w.top = take(4 * 4 * (size_t)c.n_experts);
     w.total = off;
     return w;
 }
@@ -810,7 +812,9 @@ static int32_t w4_ffn_impl(const moe_config* cfg, const W4Weights& w, const void
     a.xu = at<float>(ws, W.xu);
     a.hq = at<uint8_t>(ws, W.hq);
     a.hu = at<float>(ws, W.hu);
-    a.h = at<__nv_bfloat16>(ws, L.h);
+    a.h = at<void>(ws, L.h);
+    a.wexp = at<int8_t>(ws, W.wexp);
+    a.top = at<int32_t>(ws, W.top);
     a.ye = static_cast<__nv_bfloat16*>(ye);
     a.part = at<float>(ws, W.part);
     a.count = at<int32_t>(ws, L.w4_count);

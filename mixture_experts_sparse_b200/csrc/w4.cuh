@@ -46,7 +46,9 @@ struct W4FfnArgs {
     float* xu;             // [R_cap][w4_padded(d) / 64]: their units
     uint8_t* hq;           // [R_cap][w4_padded(d_ff)] x 2 bytes: H
     float* hu;
-    __nv_bfloat16* h;      // [R_cap, d_ff]: H, many rows
+    void* h;               // [R_cap, d_ff] fp16: H, many rows (whose x is in xq, exponents in xu, hu)
+    int8_t* wexp;          // [N, d_ff] twice and [N, d]: the weight rows' exponents
+    int32_t* top;          // [4][N]
     __nv_bfloat16* ye;     // [R_cap, d]
     float* part;           // w4_part_bytes(): sums of tiles that CTAs share
     int32_t* count;        // [2][kW4Counters], zero between calls

@@ -5,31 +5,38 @@
 //
 // The weights are the A operand: a tile is 128 weight rows by up to 192 tokens, so
 // each word is decoded once for 192 tokens, and a thread that decodes owns one
-// row.  Decoded words are bf16 integers, exact, and go straight into TMEM
-// (tcgen05.st), from where tcgen05.mma reads A: through shared memory the
-// operand would be written and read again beside the tokens' tiles, more than the
-// 128 bytes a cycle that shared memory has.  The scales do not enter the operands
-// (q s has up to 12 significant bits, bf16 8): the products of one group
-// accumulate in TMEM from zero, and a thread per weight row adds them, times the
-// row's scale, to its fp32 sums in registers -- one fma per output and group.
-// H is rounded to bf16 between the stages, as in the layer on bf16 weights.
+// row.  Decoded words go straight into TMEM (tcgen05.st), from where tcgen05.mma
+// reads A: through shared memory the operand would be written and read again
+// beside the tokens' tiles, more than the 128 bytes a cycle shared memory has.
 //
-// Bound: the instructions around the MMAs.  A block of 128 rows x 128 of K is 860
-// warp instructions to decode and, with 192 tokens, about 1100 to add up, for MMAs
-// of 800 cycles; hence the wide tile (all 512 columns of TMEM: two partial
-// accumulators of 192, two A buffers of 64), and 96 sums per adding thread, whose
-// registers setmaxnreg takes from the other warps.  Single-lane branches around
-// TMA, MMA and commit use elect.sync in a warp-uniform loop: with `lane == 0` each
-// such instruction took 45 cycles to issue instead of 9.
+// Operands are fp16, because q s (three bits times a bf16 scale's eight) is exact in
+// its eleven and not in bf16's eight; everything then accumulates over all of K in
+// TMEM.  (bf16 integers as A, with every group's sum read back from TMEM and scaled
+// in registers, ran at 0.98 ms where this takes 0.5: reading back was the
+// bottleneck.)  fp16's range is met by powers of two, which round nothing:
+//   weights: per row, so that its largest scale lies in [2^11, 2^12) -- exact for
+//     scales down to 2^-28 of it;
+//   x: per token, so that its largest value lies in [2^14, 2^15) -- exact for values
+//     down to 2^-29 of it (bf16 has eight bits);
+//   H: per token, from |u| <= sum |x w| <= K max|x| 8 max|s| and the biases, which no
+//     value passes.  The bound is about 2^10 (SwiGLU: 2^20) above typical values, whose
+//     fp16 form still has all its bits 2^8 below them, and 2^-12 is a sixteenth of the
+//     rounding to bf16 that the layer on bf16 weights applies here.
+// The epilogues undo the powers in fp32.
+//
+// Single-lane branches around TMA, MMA and commit use elect.sync in a warp-uniform
+// loop: with `lane == 0` each such instruction took 45 cycles to issue, not 9.
 //
 // Roles (five warpgroups): warp 0 TMA of the tokens' rows, 1 MMA issue, 2 TMA of
 // the packed rows and scales (they come from HBM and are asked for further ahead);
-// warps 4-11 decode, in turns, one group per A buffer; warps 12-19 add up and
-// write out, 96 tokens a group.  SwiGLU puts a feature's W1 row on lane l < 16 and
-// its W3 row on lane l + 16 of the same warp, so the gate and the value meet by a
-// shuffle.
+// warps 4-11 decode, half of every block per group; warps 12-19 write out, 96 tokens
+// a group, while the next tile accumulates in the other half of TMEM.  SwiGLU puts
+// a feature's W1 row on lane l < 16 and its W3 row on lane l + 16 of the same warp,
+// so the gate and the value meet by a shuffle.
 // Every wait is bounded; on expiry the kernel latches MOE_ERR_TIMEOUT, stops
 // issuing, waits (bounded) for its copies and MMAs, frees TMEM and returns.
+#include <cuda_fp16.h>
+
 #include "tc_common.cuh"
 #include "w4.cuh"
 
@@ -37,10 +44,9 @@ namespace moe {
 using namespace tc;
 namespace {
 
-constexpr int kAddGroups = 2;                     // warpgroups that add up
-constexpr int kThreadsTc = 128 * (3 + kAddGroups);
+constexpr int kThreadsTc = 640;
 constexpr int kTileN = 192;                       // tokens of a tile
-constexpr int kPartN = kTileN / kAddGroups;       // ... of a group of adding warps
+constexpr int kPartN = kTileN / 2;                // ... of a group of writing warps
 constexpr int kBoxN = 32;                         // tokens per TMA box
 constexpr int kWStages = 4;                       // packed rows and scales: 256 of K each
 constexpr int kXStages = 3;                       // tokens: 128 of K each
@@ -50,14 +56,7 @@ constexpr int kXBytes = 2 * kXSub;
 constexpr int kSBytes = 2048;                     // scales of a stage: 2 boxes x 256 / G groups x 64 rows
 constexpr int kSmemTc = kWStages * (kWBytes + kSBytes) + kXStages * kXBytes + 1024;
 constexpr uint32_t kColD = 0, kColA = 2 * kTileN; // TMEM columns
-// Registers per thread: the launch's 640 x 96 are dealt out anew, 40 + 2 x 72 +
-// 2 x 144 = 472 <= 5 x 96 per warpgroup lane.
-constexpr int kRegsLaunch = 96, kRegsControl = 32, kRegsDecode = 64, kRegsAdd = 160;
-static_assert(kRegsControl + 2 * kRegsDecode + kAddGroups * kRegsAdd <= (3 + kAddGroups) * kRegsLaunch, "register pool");
-template <int R>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
-template <int R>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+constexpr int kNanExp = 0x7FFF;                   // exponent of a row that holds a NaN or infinity
 
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
 
@@ -65,7 +64,11 @@ struct TcParams {
     const int32_t* offsets; int N; int64_t R_cap;
     int m_dim, k_dim;
     const __nv_bfloat16* bias_a; const __nv_bfloat16* bias_b;
-    __nv_bfloat16* out;           // [R, m_dim]
+    const int8_t* ea; const int8_t* eb;   // [N, m_dim] row exponents: scales were taken times 2^-e
+    const int16_t* ex;                    // [R] exponents of the tokens' rows: x times 2^-ex
+    const int32_t* top;                   // stage 1: [4][N] largest scale and bias of W1, W3 (as float bits)
+    int16_t* eh;                          // stage 1: [R] exponents of H
+    void* out;                            // stage 1: H [R, m_dim] fp16, stage 2: y [R, m_dim] bf16
     int32_t* status;
     long long limit_ns;
 };
@@ -85,21 +88,6 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// two fp32 fused multiply-adds in one instruction
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
 // one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
@@ -107,27 +95,46 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Weights 2 p and 2 p + 1 of a word's eight as a bf16 pair of integers: 128 + (q + 8)
-// is exact in bf16 (0x4300 is 128, whose last place is 1), and so is the difference.
-__device__ __forceinline__ uint32_t decode_pair(uint32_t w, int p) {
+// Weights 2 p and 2 p + 1 of a word's eight, times the scale s2 (an fp16 pair):
+// 0x6400 is 1024 in fp16, whose last place is 1, so nibbles in the low bits add to it
+// exactly, and in bits 4-7 as sixteenfold; w8 = w >> 8 holds the odd pairs.
+__device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t w8, int p, __half2 s2) {
     uint32_t u;   // one operation: written as two immediates it would be two
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(w >> (4 * p)), "r"(0x000F000Fu), "r"(0x43004300u));
-    const uint32_t c = 0x43084308u;   // 136, 136
-    const __nv_bfloat162 r =
-        __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&u), *reinterpret_cast<const __nv_bfloat162*>(&c));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(u) : "r"(p < 2 ? w : w8), "r"(p & 1 ? 0x00F000F0u : 0x000F000Fu), "r"(0x64006400u));
+    __half2 q = *reinterpret_cast<const __half2*>(&u);
+    if (p & 1) q = __hfma2(q, __half2half2(__ushort_as_half(0x2C00)), __half2half2(__ushort_as_half(0xD480)));   // / 16 - 72
+    else q = __hsub2(q, __half2half2(__ushort_as_half(0x6408)));                                                 // - 1032
+    q = __hmul2(q, s2);
+    return *reinterpret_cast<const uint32_t*>(&q);
+}
+
+// 2^e for -126 <= e <= 127 (others clamped: 0 < 2^e < inf)
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+// exponent of a finite positive float's leading bit (0 and subnormals: -127)
+__device__ __forceinline__ int exp_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
+
+// 2^ex times this brings x to fp16 range; the exponent of the bound on |H| of a token
+template <int EPI>
+__device__ __forceinline__ int h_exponent(const int32_t* top, int N, int e, int ex, int k_dim) {
+    // |u| < 2^(ex + 15) k_dim 8 2^(exp(max scale) + 1), plus the bias
+    const int kbits = 32 - __clz(k_dim - 1);
+    auto side = [&](int m) {
+        const int u = ex + 15 + kbits + 3 + exp_of(top[2 * m * N + e]) + 1, b = exp_of(top[(2 * m + 1) * N + e]) + 1;
+        return max(u, b) + 1;
+    };
+    return min(max(side(0) + (EPI == W4_SWIGLU ? side(1) : 0) - 15, -126), 126);
 }
 
 struct SharedTc {
-    uint64_t wfull[kWStages], wempty[kWStages], sempty[kWStages];   // wfull: rows and scales
+    uint64_t wfull[kWStages], wempty[kWStages];
     uint64_t xfull[kXStages], xempty[kXStages];
-    uint64_t afull[2];              // a block's weights are in TMEM
-    uint64_t mdone[2];              // its MMAs are done: A is free, (G = 128) its sums are there
-    uint64_t dfull[2], dempty[2];   // partial accumulators; dfull: G < 128
+    uint64_t afull[2], mdone[2];    // a block's weights are in TMEM; its MMAs are done
+    uint64_t dfull[2], dempty[2];   // accumulators of a tile
     uint64_t done;
     uint32_t tmem;
     int abort, live;
     int row[129], exp[128], first[129];
+    float scale[8][2][kPartN];      // per writing warp: the tokens' powers of two
 };
 
 struct Tile {
@@ -175,7 +182,6 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(smem_u32(&sh.wfull[s]), 1);
             mbar_init(smem_u32(&sh.wempty[s]), 8);
-            mbar_init(smem_u32(&sh.sempty[s]), 4 * kAddGroups);
         }
         for (int s = 0; s < kXStages; ++s) {
             mbar_init(smem_u32(&sh.xfull[s]), 1);
@@ -185,7 +191,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             mbar_init(smem_u32(&sh.afull[i]), 8);
             mbar_init(smem_u32(&sh.mdone[i]), 1);
             mbar_init(smem_u32(&sh.dfull[i]), 1);
-            mbar_init(smem_u32(&sh.dempty[i]), 4 * kAddGroups);
+            mbar_init(smem_u32(&sh.dempty[i]), 8);
         }
         mbar_init(smem_u32(&sh.done), 1);
         sh.abort = 0;
@@ -243,7 +249,6 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const Waiter w{&sh.abort, p.status, p.limit_ns};
 
     if (warp < 4) {
-        regs_dec<kRegsControl>();
         if (warp == 0) {
             // ---------------- TMA: the tokens' rows ----------------
             int xs = 0;
@@ -286,8 +291,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 const int row = t.e * p.m_dim + t.m0;
                 const bool second = MATS == 2 || t.m0 + 64 < p.m_dim;   // the upper 64 rows hold something
                 for (int kb = 0; kb < nb; kb += 2) {
-                    ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wempty[ws]), wph ^ 1u, w) &&
-                                                     wait_bar_soon(smem_u32(&sh.sempty[ws]), wph ^ 1u, w));
+                    ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wempty[ws]), wph ^ 1u, w));
                     if (!ok) break;
                     constexpr int SB = 2 * PER * 128;   // one box of scales
                     const uint32_t fb = smem_u32(&sh.wfull[ws]), dst = smem_u32(smem) + ws * kWBytes;
@@ -321,37 +325,28 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const uint64_t bd0 = umma_desc(smem_u32(smem_x));
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const Tile t = tile_of(sh, u, FEATS);
-                const uint32_t idesc = idesc_bf16_f32(128, (t.n + 15) / 16 * 16);
-                for (int kb = 0; kb < nb && ok; ++kb) {
+                const uint32_t idesc = idesc_f16_f32(128, (t.n + 15) / 16 * 16);
+                if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.dempty[d]), dph ^ 1u, w)))) break;
+                const uint32_t dd = tmem + kColD + d * kTileN;
+                for (int kb = 0; kb < nb; ++kb) {
                     ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.afull[a]), aph, w) &&
                                                      wait_bar_soon(smem_u32(&sh.xfull[xs]), xph, w));
                     if (!ok) break;
+                    tc_fence_after();
+                    issued = true;
                     const uint64_t bd = bd0 + (uint64_t)(xs * (kXBytes >> 4));
                     const uint32_t ad = tmem + kColA + a * 64;
                     const int nk = min(8, (p.k_dim - kb * kW4Block) / 16);   // K is a multiple of 16
+                    if (elect_one()) {
 #pragma unroll
-                    for (int gi = 0; gi < PER; ++gi) {
-                        if (gi * (8 / PER) >= nk) break;
-                        if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.dempty[d]), dph ^ 1u, w)))) break;
-                        tc_fence_after();
-                        issued = true;
-                        const uint32_t dd = tmem + kColD + d * kTileN;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int kk = gi * (8 / PER); kk < (gi + 1) * (8 / PER); ++kk)
-                                if (kk < nk)
-                                    umma_ts(dd, ad + 8 * kk, bd + (uint64_t)((kk / 4 * kXSub) >> 4) + 2 * (kk % 4), idesc,
-                                            kk > gi * (8 / PER));
-                            if (PER > 1) umma_commit(smem_u32(&sh.dfull[d]));
-                            if (gi == PER - 1 || (gi + 1) * (8 / PER) >= nk) {
-                                umma_commit(smem_u32(&sh.mdone[a]));
-                                umma_commit(smem_u32(&sh.xempty[xs]));
-                            }
-                        }
-                        __syncwarp();
-                        d ^= 1;
-                        if (d == 0) dph ^= 1u;
+                        for (int kk = 0; kk < 8; ++kk)
+                            if (kk < nk)
+                                umma_ts(dd, ad + 8 * kk, bd + (uint64_t)((kk / 4 * kXSub) >> 4) + 2 * (kk % 4), idesc, kb | kk);
+                        umma_commit(smem_u32(&sh.mdone[a]));
+                        umma_commit(smem_u32(&sh.xempty[xs]));
+                        if (kb + 1 == nb) umma_commit(smem_u32(&sh.dfull[d]));
                     }
+                    __syncwarp();
                     a ^= 1;
                     if (a == 0) aph ^= 1u;
                     if (++xs == kXStages) {
@@ -359,6 +354,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                         xph ^= 1u;
                     }
                 }
+                d ^= 1;
+                if (d == 0) dph ^= 1u;
             }
             if (issued) {   // every MMA has completed before TMEM is freed
                 if (elect_one()) umma_commit(smem_u32(&sh.done));
@@ -371,28 +368,39 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // two groups of four warps, half of every block each: the words t = 2 h, 2 h + 1,
         // columns 16 j + 8 h .. + 7.  They decode into registers before they wait for
         // the A buffer, so only the stores are between one MMA and the next but one.
-        regs_dec<kRegsDecode>();
         const int quad = warp & 3;   // TMEM lane quadrant
         const int h = (warp - 4) >> 2;
         // SwiGLU: lanes 0-15 hold 16 features of W1, lanes 16-31 the same of W3
         const int r = MATS == 2 ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
+        // its scales in a stage: box, then 64 features a group
+        const int soff = ((r >> 6) * (2 * PER * 64) + (r & 63)) * 2;
+        const int8_t* exps = MATS == 2 && lane >= 16 ? p.eb : p.ea;
         int ws = 0, a = 0;
         uint32_t wph = 0, aph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Tile t = tile_of(sh, u, FEATS);
+            const int feat = t.m0 + (MATS == 2 ? r & 63 : r);
+            const float down = pow2i(feat < p.m_dim ? -(int)exps[(int64_t)t.e * p.m_dim + feat] : 0);
             for (int kb = 0; kb < nb && ok; ++kb) {
                 if (kb % 2 == 0) ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w));
                 if (!ok) break;
                 const uint8_t* src = smem + ws * kWBytes + r * 128;
+                const uint8_t* ssrc = smem_s + ws * kSBytes + kb % 2 * (PER * 128) + soff;
+                __half2 sc[PER];
+#pragma unroll
+                for (int g = 0; g < PER; ++g)
+                    sc[g] = __float2half2_rn(
+                        __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(ssrc + g * 128) << 16) * down);
                 uint32_t v[32];
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + 2 * h + t) ^ (r & 7)) << 4));
+                for (int t2 = 0; t2 < 2; ++t2) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + 2 * h + t2) ^ (r & 7)) << 4));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t word = j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[8 * j + 4 * t + i] = decode_pair(word, i);
+                        for (int i = 0; i < 4; ++i) v[8 * j + 4 * t2 + i] = decode_pair(word, word >> 8, i, sc[j * PER / 4]);
                     }
                 }
                 if (kb % 2 == 1 || kb + 1 == nb) {   // this warp is done with the stage
@@ -417,105 +425,160 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             }
         }
     } else {
-        // ---------------- add up and write out: lane = weight row ----------------
+        // ---------------- write out: lane = weight row ----------------
         // two groups of four warps, 96 of the tile's tokens each
-        regs_inc<kRegsAdd>();
         const int quad = warp & 3, c0 = (warp - 12) / 4 * kPartN;
         const int f = MATS == 2 ? quad * 16 + (lane & 15) : quad * 32 + lane;   // feature of the tile
-        // its scales in a stage: box, then 64 features a group
-        const int soff = (MATS == 2 ? (lane >> 4) * (2 * PER * 64) + f : f / 64 * (2 * PER * 64) + f % 64) * 2;
-        const __nv_bfloat16* bias = MATS == 2 && lane >= 16 ? p.bias_b : p.bias_a;
-        const int ng = (p.k_dim + G - 1) / G;
-        int d = 0, ws = 0;
-        uint32_t dph = 0, wph = 0;
+        const bool low = lane < 16;
+        const __nv_bfloat16* bias = MATS == 2 && !low ? p.bias_b : p.bias_a;
+        const int8_t* exps = MATS == 2 && !low ? p.eb : p.ea;
+        int d = 0;
+        uint32_t dph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const Tile t = tile_of(sh, u, FEATS);
             const int feat = t.m0 + f;
             const bool in = feat < p.m_dim;
             const int n = t.n - c0;   // this group's tokens (may be none)
-            uint64_t acc2[kPartN / 2];   // pairs of fp32 sums (fma.rn.f32x2)
-#pragma unroll
-            for (int c = 0; c < kPartN / 2; ++c) acc2[c] = 0;
-            for (int g = 0; g < ng; ++g) {
-                const int gs = g % (2 * PER);   // group of the stage
-                if (gs == 0 && !(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w)))) break;
-                const float s = __uint_as_float(
-                    (uint32_t)*reinterpret_cast<const uint16_t*>(smem_s + ws * kSBytes + gs * 128 + soff) << 16);
-                if (gs == 2 * PER - 1 || g + 1 == ng) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.sempty[ws]));
-                    if (++ws == kWStages) {
-                        ws = 0;
-                        wph ^= 1u;
-                    }
+            const int64_t at = (int64_t)t.e * p.m_dim + feat;
+            const float up = pow2i(in ? exps[at] : 0);
+            const float b = in && bias ? __bfloat162float(bias[at]) : 0.f;
+            // the powers of two of these tokens: x's, and H's
+            float* s_x = sh.scale[warp - 12][0];
+            float* s_h = sh.scale[warp - 12][1];
+            for (int c = lane; c < n && c < kPartN; c += 32) {
+                const int ex = p.ex[t.row0 + c0 + c];
+                s_x[c] = ex == kNanExp ? __int_as_float(0x7FC00000) : pow2i(ex);
+                if (EPI != W4_OUT) {
+                    const int eh = h_exponent<EPI>(p.top, p.N, t.e, ex, p.k_dim);
+                    s_h[c] = pow2i(-eh);
+                    if (t.m0 == 0 && quad == 0) p.eh[t.row0 + c0 + c] = (int16_t)(ex == kNanExp ? kNanExp : eh);
                 }
-                ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(PER > 1 ? &sh.dfull[d] : &sh.mdone[d]), dph, w));
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t src = tmem + kColD + d * kTileN + c0 + ((uint32_t)(quad * 32) << 16);
-                const uint64_t s2 = pack_f32x2(s, s);
-                auto release = [&]() {   // this warp's last read of the buffer
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.dempty[d]));
-                };
-                if (n <= 0) release();
-#pragma unroll
-                for (int c = 0; c < kPartN / 32; ++c) {
-                    if (32 * c < n) {
-                        uint32_t v[32];
-                        tmem_ld32(src + 32 * c, v);
-                        tmem_wait_ld();
-                        if (32 * (c + 1) >= n || c + 1 == kPartN / 32) release();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            acc2[16 * c + i] = fma_f32x2(pack_f32x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), s2,
-                                                         acc2[16 * c + i]);
-                    }
-                }
-                d ^= 1;
-                if (d == 0) dph ^= 1u;
             }
-            if (!ok) break;
-            float acc[kPartN];
+            __syncwarp();
+            if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.dfull[d]), dph, w)))) break;
+            tc_fence_after();
+            const uint32_t src = tmem + kColD + d * kTileN + c0 + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+            for (int cb = 0; cb < kPartN && cb < n; cb += 32) {
+                uint32_t v[32];
+                tmem_ld32(src + cb, v);
+                tmem_wait_ld();
+                const int64_t row = (int64_t)(t.row0 + c0 + cb) * p.m_dim + feat;
+                if (EPI == W4_SWIGLU) {
+                    // lanes < 16 finish the even tokens, their partners the odd ones
+                    __half* dst = reinterpret_cast<__half*>(p.out) + row + (low ? 0 : p.m_dim);
 #pragma unroll
-            for (int c = 0; c < kPartN / 2; ++c) unpack_f32x2(acc2[c], acc[2 * c], acc[2 * c + 1]);
-            const float b = in && bias ? __bfloat162float(bias[(int64_t)t.e * p.m_dim + feat]) : 0.f;
-            __nv_bfloat16* dst = p.out + (int64_t)(t.row0 + c0) * p.m_dim + feat;
-            if (EPI == W4_SWIGLU) {
-                // lanes < 16 finish the even tokens, their partners the odd ones
-                const bool low = lane < 16;
-                if (!low) dst += p.m_dim;
-#pragma unroll
-                for (int c = 0; c < kPartN; c += 2) {
-                    if (c < n) {   // (a break would put acc in local memory)
-                        const float mine = (low ? acc[c] : acc[c + 1]) + b, send = (low ? acc[c + 1] : acc[c]) + b;
-                        const float other = __shfl_xor_sync(0xffffffffu, send, 16);
-                        const float gate = low ? mine : other, up = low ? other : mine;
+                    for (int c = 0; c < 32; c += 2) {
+                        const float v0 = fmaf(__uint_as_float(v[c]) * up, s_x[cb + c], b);
+                        const float v1 = fmaf(__uint_as_float(v[c + 1]) * up, s_x[cb + c + 1], b);
+                        const float other = __shfl_xor_sync(0xffffffffu, low ? v1 : v0, 16);
+                        const float gate = low ? v0 : other, val = low ? other : v1;
                         // e^-z -> inf for very negative z: the fast division gives the limit 0
-                        const float o = __fdividef(gate, 1.f + fast_exp2(-gate * kLog2e)) * up;
-                        if (in && (low || c + 1 < n)) *dst = __float2bfloat16_rn(o);
-                        dst += 2 * p.m_dim;
+                        const float o = __fdividef(gate, 1.f + fast_exp2(-gate * kLog2e)) * val;
+                        if (in && cb + c + (low ? 0 : 1) < n)
+                            dst[(int64_t)c * p.m_dim] = __float2half_rn(o * s_h[cb + c + (low ? 0 : 1)]);
                     }
-                }
-            } else {
+                } else {
 #pragma unroll
-                for (int c = 0; c < kPartN; ++c) {
-                    if (c < n) {
-                        float o = acc[c] + b;
-                        if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
-                        if (in) *dst = __float2bfloat16_rn(o);
-                        dst += p.m_dim;
+                    for (int c = 0; c < 32; ++c) {
+                        float o = fmaf(__uint_as_float(v[c]) * up, s_x[cb + c], b);
+                        if (EPI == W4_RELU) {
+                            o = o < 0.f ? 0.f : o;   // NaN stays
+                            if (in && cb + c < n)
+                                (reinterpret_cast<__half*>(p.out) + row)[(int64_t)c * p.m_dim] = __float2half_rn(o * s_h[cb + c]);
+                        } else if (in && cb + c < n) {
+                            (reinterpret_cast<__nv_bfloat16*>(p.out) + row)[(int64_t)c * p.m_dim] = __float2bfloat16_rn(o);
+                        }
                     }
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_relaxed(smem_u32(&sh.dempty[d]));
+            d ^= 1;
+            if (d == 0) dph ^= 1u;
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// x as fp16 rows, each times a power of two (one warp per row); clears `top`.
+__global__ void __launch_bounds__(256)
+w4_half_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ offsets, int N, int64_t R_cap,
+                    int k_dim, __half* __restrict__ out, int16_t* __restrict__ ex, int32_t* __restrict__ top) {
+    pdl_wait();
+    pdl_launch();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < 4 * N; i += 256) top[i] = 0;
+    const int64_t last = offsets[N], rows = last < 0 ? 0 : (last > R_cap ? R_cap : last);
+    const int lane = threadIdx.x & 31;
+    for (int64_t r = (int64_t)blockIdx.x * 8 + threadIdx.x / 32; r < rows; r += (int64_t)gridDim.x * 8) {
+        const uint4* src = reinterpret_cast<const uint4*>(x + r * k_dim);
+        uint32_t m = 0;   // bf16 magnitudes of both halves, compared as 16-bit integers
+        for (int i = lane; i < k_dim / 8; i += 32) {
+            const uint4 q = src[i];
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu), __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu)));
+        }
+        const uint32_t big = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu)) << 16;
+        const bool finite = big < 0x7F800000u;
+        const int e = max(exp_of(big) - 14, -112);
+        const float down = finite ? pow2i(-e) : 0.f;
+        if (lane == 0) ex[r] = (int16_t)(finite ? e : kNanExp);
+        uint4* dst = reinterpret_cast<uint4*>(out + r * k_dim);
+        for (int i = lane; i < k_dim / 8; i += 32) {
+            const uint4 q = finite ? src[i] : make_uint4(0, 0, 0, 0);
+            const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __half2 hh = __floats2half2_rn(bf16lo(in[k]) * down, bf16hi(in[k]) * down);
+                o[k] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// Every weight row's exponent: its largest finite scale times 2^-e lies in [2^11, 2^12);
+// and of W1, W3 the largest scale and bias of the expert.  One thread per row.
+struct ExpArgs {
+    const uint16_t* s[3]; int8_t* e[3];
+    const __nv_bfloat16* b[2];
+    int rows[3], ng[3];
+    const int32_t* offsets; int N;
+    int32_t* top;
+};
+__global__ void __launch_bounds__(256)
+w4_exponent_kernel(const ExpArgs a) {
+    pdl_wait();
+    pdl_launch();
+    const int m = blockIdx.z, e = blockIdx.y, row = blockIdx.x * 256 + threadIdx.x;
+    if (a.s[m] == nullptr || a.offsets[e + 1] <= a.offsets[e]) return;   // no such matrix, no rows for the expert
+    uint32_t big = 0, bias = 0;
+    if (row < a.rows[m]) {
+        const uint16_t* s = a.s[m] + (int64_t)e * a.ng[m] * a.rows[m] + row;
+#pragma unroll 8
+        for (int g = 0; g < a.ng[m]; ++g) {
+            const uint32_t v = s[(int64_t)g * a.rows[m]] & 0x7FFFu;
+            big = max(big, v < 0x7F80u ? v : 0u);
+        }
+        a.e[m][(int64_t)e * a.rows[m] + row] = (int8_t)max(exp_of(big << 16) - 11, -126);
+        if (m < 2 && a.b[m]) {
+            const uint32_t v = __bfloat16_as_ushort(a.b[m][(int64_t)e * a.rows[m] + row]) & 0x7FFFu;
+            bias = v < 0x7F80u ? v : 0u;
+        }
+    }
+    if (m == 2) return;
+    big = __reduce_max_sync(0xffffffffu, big);
+    bias = __reduce_max_sync(0xffffffffu, bias);
+    if ((threadIdx.x & 31) == 0) {   // a maximum: the order of arrival does not matter
+        atomicMax(a.top + 2 * m * a.N + e, (int32_t)(big << 16));
+        atomicMax(a.top + (2 * m + 1) * a.N + e, (int32_t)(bias << 16));
+    }
 }
 
 template <int EPI, int G>
@@ -555,16 +618,52 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     Maps m1, m3, m2;
     CUtensorMap mx, mh;
     if (!m1.make(a.w1, a.N, a.d_ff, a.d, a.group) || !m2.make(a.w2, a.N, a.d, a.d_ff, a.group) ||
-        !make_map_bf16(&mx, a.xe, a.R_cap, a.d, kBoxN) || !make_map_bf16(&mh, a.h, a.R_cap, a.d_ff, kBoxN))
+        !make_map_bf16(&mx, a.xq, a.R_cap, a.d, kBoxN) || !make_map_bf16(&mh, a.h, a.R_cap, a.d_ff, kBoxN))
         return cudaErrorInvalidValue;
     m3 = m1;
-    if (a.act == MOE_SWIGLU && !m3.make(a.w3, a.N, a.d_ff, a.d, a.group)) return cudaErrorInvalidValue;
+    const bool swiglu = a.act == MOE_SWIGLU;
+    if (swiglu && !m3.make(a.w3, a.N, a.d_ff, a.d, a.group)) return cudaErrorInvalidValue;
+    // exponents: x's and H's in the place of the few-row kernels' units, the weights' in their own
+    int16_t* ex = reinterpret_cast<int16_t*>(a.xu);
+    int16_t* eh = reinterpret_cast<int16_t*>(a.hu);
+    int8_t* e1 = a.wexp;
+    int8_t* e3 = e1 + (int64_t)a.N * a.d_ff;
+    int8_t* e2 = e3 + (int64_t)a.N * a.d_ff;
+    const int64_t rb = (a.R_cap + 7) / 8;
+    err = launch_k(w4_half_rows_kernel, dim3((unsigned)(rb < 8 * sms ? rb : 8 * sms)), dim3(256), 0, s, 1, a.xe, a.offsets,
+                   a.N, a.R_cap, a.d, reinterpret_cast<__half*>(a.xq), ex, a.top);
+    if (err != cudaSuccess) return err;
+    ExpArgs ea{};
+    const int ng1 = (a.d + a.group - 1) / a.group, ng2 = (a.d_ff + a.group - 1) / a.group;
+    ea.s[0] = a.w1.s;
+    ea.s[1] = swiglu ? a.w3.s : nullptr;
+    ea.s[2] = a.w2.s;
+    ea.e[0] = e1;
+    ea.e[1] = e3;
+    ea.e[2] = e2;
+    ea.b[0] = a.b1;
+    ea.b[1] = a.b3;
+    ea.rows[0] = ea.rows[1] = a.d_ff;
+    ea.rows[2] = a.d;
+    ea.ng[0] = ea.ng[1] = ng1;
+    ea.ng[2] = ng2;
+    ea.offsets = a.offsets;
+    ea.N = a.N;
+    ea.top = a.top;
+    const int most = a.d > a.d_ff ? a.d : a.d_ff;
+    err = launch_k(w4_exponent_kernel, dim3((unsigned)((most + 255) / 256), (unsigned)a.N, 3u), dim3(256), 0, s, 1, ea);
+    if (err != cudaSuccess) return err;
     TcParams p{};
     p.offsets = a.offsets;
     p.N = a.N;
     p.R_cap = a.R_cap;
     p.status = &a.hdr->status;
     p.limit_ns = kWaitLimitNs;
+    p.ea = e1;
+    p.eb = e3;
+    p.ex = ex;
+    p.eh = eh;
+    p.top = a.top;
     p.m_dim = a.d_ff;
     p.k_dim = a.d;
     p.bias_a = a.b1;
@@ -577,6 +676,8 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     p.k_dim = a.d_ff;
     p.bias_a = a.b2;
     p.bias_b = nullptr;
+    p.ea = e2;
+    p.ex = eh;
     p.out = a.ye;
     return run_tc<W4_OUT>(m2, m2, mh, p, a.group, sms, s);
 }
