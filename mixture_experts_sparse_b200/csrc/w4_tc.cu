@@ -81,10 +81,16 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]),
+        "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]),
+        "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -188,7 +194,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             mbar_init(smem_u32(&sh.xempty[s]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.afull[i]), 8);
+            mbar_init(smem_u32(&sh.afull[i]), 4);
             mbar_init(smem_u32(&sh.mdone[i]), 1);
             mbar_init(smem_u32(&sh.dfull[i]), 1);
             mbar_init(smem_u32(&sh.dempty[i]), 8);
@@ -365,63 +371,69 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
     } else if (warp < 12) {
         // ---------------- decode: lane = weight row ----------------
-        // two groups of four warps, half of every block each: the words t = 2 h, 2 h + 1,
-        // columns 16 j + 8 h .. + 7.  They decode into registers before they wait for
-        // the A buffer, so only the stores are between one MMA and the next but one.
+        // Two groups of four warps take blocks in turn, one for each A buffer, and
+        // decode into registers before they wait for it: only the stores lie between
+        // one MMA and the next but one.  (Each barrier operation costs a warp about
+        // 130 cycles; halves of every block, twice as many of them, took 1280 cycles
+        // a block.)
         const int quad = warp & 3;   // TMEM lane quadrant
-        const int h = (warp - 4) >> 2;
+        const int a = (warp - 4) >> 2;
         // SwiGLU: lanes 0-15 hold 16 features of W1, lanes 16-31 the same of W3
         const int r = MATS == 2 ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
         // its scales in a stage: box, then 64 features a group
         const int soff = ((r >> 6) * (2 * PER * 64) + (r & 63)) * 2;
         const int8_t* exps = MATS == 2 && lane >= 16 ? p.eb : p.ea;
-        int ws = 0, a = 0;
+        const uint32_t dst = tmem + kColA + a * 64 + ((uint32_t)(quad * 32) << 16);
+        int ws = 0, turn = 0;
         uint32_t wph = 0, aph = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
             const Tile t = tile_of(sh, u, FEATS);
             const int feat = t.m0 + (MATS == 2 ? r & 63 : r);
             const float down = pow2i(feat < p.m_dim ? -(int)exps[(int64_t)t.e * p.m_dim + feat] : 0);
-            for (int kb = 0; kb < nb && ok; ++kb) {
-                if (kb % 2 == 0) ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w));
-                if (!ok) break;
-                const uint8_t* src = smem + ws * kWBytes + r * 128;
-                const uint8_t* ssrc = smem_s + ws * kSBytes + kb % 2 * (PER * 128) + soff;
-                __half2 sc[PER];
+            for (int kb = 0; kb < nb && ok; ++kb, turn ^= 1) {
+                const bool mine = turn == a, last = kb % 2 == 1 || kb + 1 == nb;
+                uint32_t v[64];
+                if (mine) {
+                    if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.wfull[ws]), wph, w)))) break;
+                    const uint8_t* src = smem + ws * kWBytes + r * 128;
+                    const uint8_t* ssrc = smem_s + ws * kSBytes + kb % 2 * (PER * 128) + soff;
+                    __half2 sc[PER];
 #pragma unroll
-                for (int g = 0; g < PER; ++g)
-                    sc[g] = __float2half2_rn(
-                        __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(ssrc + g * 128) << 16) * down);
-                uint32_t v[32];
+                    for (int g = 0; g < PER; ++g)
+                        sc[g] = __float2half2_rn(
+                            __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(ssrc + g * 128) << 16) * down);
 #pragma unroll
-                for (int t2 = 0; t2 < 2; ++t2) {
-                    const uint4 q = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + 2 * h + t2) ^ (r & 7)) << 4));
+                    for (int t4 = 0; t4 < 4; ++t4) {
+                        const uint4 q = *reinterpret_cast<const uint4*>(src + (((kb % 2 * 4 + t4) ^ (r & 7)) << 4));
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t word = j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w;
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t word = j == 0 ? q.x : j == 1 ? q.y : j == 2 ? q.z : q.w;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[8 * j + 4 * t2 + i] = decode_pair(word, word >> 8, i, sc[j * PER / 4]);
+                            for (int i = 0; i < 4; ++i)
+                                v[16 * j + 4 * t4 + i] = decode_pair(word, word >> 8, i, sc[j * PER / 4]);
+                        }
                     }
-                }
-                if (kb % 2 == 1 || kb + 1 == nb) {   // this warp is done with the stage
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.wempty[ws]));
-                    if (++ws == kWStages) {
-                        ws = 0;
-                        wph ^= 1u;
+                    if (lane == 0) {   // one of the stage's two blocks, or its only one
+                        mbar_arrive(smem_u32(&sh.wempty[ws]));
+                        if (last && kb % 2 == 0) mbar_arrive(smem_u32(&sh.wempty[ws]));
                     }
                 }
+                if (last && ++ws == kWStages) {
+                    ws = 0;
+                    wph ^= 1u;
+                }
+                if (!mine) continue;
                 if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.mdone[a]), aph ^ 1u, w)))) break;
+                aph ^= 1u;
                 tc_fence_after();
-                const uint32_t dst = tmem + kColA + a * 64 + 8 * h + ((uint32_t)(quad * 32) << 16);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmem_st8(dst + 16 * j, v + 8 * j);
+                tmem_st32(dst, v);
+                tmem_st32(dst + 32, v + 32);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.afull[a]));
-                a ^= 1;
-                if (a == 0) aph ^= 1u;
+                if (lane == 0) mbar_arrive_relaxed(smem_u32(&sh.afull[a]));
             }
         }
     } else {
