@@ -47,7 +47,7 @@ namespace {
 constexpr int kThreadsTc = 640;
 constexpr int kTileN = 192;                       // tokens of a tile
 constexpr int kPartN = kTileN / 2;                // ... of a group of writing warps
-constexpr int kBoxN = 32;                         // tokens per TMA box
+constexpr int kBoxN = 64;                         // tokens per TMA box
 constexpr int kWStages = 4;                       // packed rows and scales: 256 of K each
 constexpr int kXStages = 3;                       // tokens: 128 of K each
 constexpr int kWBytes = 128 * 128;
@@ -255,27 +255,29 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     const Waiter w{&sh.abort, p.status, p.limit_ns};
 
     if (warp < 4) {
-        if (warp == 0) {
-            // ---------------- TMA: the tokens' rows ----------------
+        if (warp == 0 || warp == 3) {
+            // ---------------- TMA: the tokens' rows (two warps, blocks in turn) ----------------
             int xs = 0;
             uint32_t xph = 0, xused = 0;
-            bool ok = true;
+            bool ok = true, mine = warp == 0;
             for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
                 const Tile t = tile_of(sh, u, FEATS);
                 const int boxes = (t.n + kBoxN - 1) / kBoxN;
-                for (int kb = 0; kb < nb; ++kb) {
-                    ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.xempty[xs]), xph ^ 1u, w));
-                    if (!ok) break;
-                    const uint32_t fb = smem_u32(&sh.xfull[xs]), dst = smem_u32(smem_x) + xs * kXBytes;
-                    const int halves = kb * kW4Block + 64 < p.k_dim ? 2 : 1;
-                    if (elect_one()) {
-                        mbar_expect_tx(fb, halves * boxes * kBoxN * 128);
-                        for (int h = 0; h < halves; ++h)
-                            for (int b = 0; b < boxes; ++b)
-                                tma_load_2d(dst + h * kXSub + b * kBoxN * 128, &map_x, fb, kb * kW4Block + h * 64,
-                                            t.row0 + b * kBoxN);
+                for (int kb = 0; kb < nb; ++kb, mine = !mine) {
+                    if (mine) {
+                        ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.xempty[xs]), xph ^ 1u, w));
+                        if (!ok) break;
+                        const uint32_t fb = smem_u32(&sh.xfull[xs]), dst = smem_u32(smem_x) + xs * kXBytes;
+                        const int halves = kb * kW4Block + 64 < p.k_dim ? 2 : 1;
+                        if (elect_one()) {
+                            mbar_expect_tx(fb, halves * boxes * kBoxN * 128);
+                            for (int h = 0; h < halves; ++h)
+                                for (int b = 0; b < boxes; ++b)
+                                    tma_load_2d(dst + h * kXSub + b * kBoxN * 128, &map_x, fb, kb * kW4Block + h * 64,
+                                                t.row0 + b * kBoxN);
+                        }
+                        __syncwarp();
                     }
-                    __syncwarp();
                     xused |= 1u << xs;
                     if (++xs == kXStages) {
                         xs = 0;
@@ -283,7 +285,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     }
                 }
             }
-            // every load has landed before the CTA retires
+            // every load has landed before the CTA retires (each warp looks at all stages)
             for (int s = 0; s < kXStages; ++s)
                 if (xused >> s & 1u) drain_bar(smem_u32(&sh.xfull[s]), s < xs ? xph : xph ^ 1u, p.limit_ns, p.status);
         } else if (warp == 2) {
