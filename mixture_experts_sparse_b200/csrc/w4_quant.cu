@@ -1,14 +1,19 @@
 // 4-bit quantisation of weight matrices with a scale per group of G weights of a
 // row, and back.
 //   scale = bf16(max |w| / 7),  q = rint(w / scale) in [-7, 7],  value = q scale.
-// Both are decided exactly, whatever the fp32 quotient rounds to: a quotient
-// that lands on a tie is settled by the sign of its fma residual, so the result
-// is that of real arithmetic with ties to even.  A group of zeros has scale 0;
-// a group with an infinity or NaN has scale NaN and stands for NaN as a whole.
+// Both are decided exactly, whatever a quotient in fp32 rounds to, so the result is
+// that of real arithmetic with ties to even.  For q: r = rint(w / s) from an
+// approximate quotient is at most one off, and the residual w - r s is exact in one
+// fma (r s has 12 bits, and what is left of w is a multiple of its last place and
+// below s); r is right iff |w - r s| < s / 2, and only the lanes' 8 weights for which
+// that fails, ties among them, take the long way.  A group of zeros has scale 0; a
+// group with an infinity or NaN has scale NaN and stands for NaN as a whole.
 //
-// Bound by HBM: one read of the weights, half a byte plus 2 / G written each.  A
-// lane owns eight consecutive weights (one word of the packed row), sixteen
-// lanes a block of 128; several blocks are in flight per lane.
+// Bound by HBM: one read of the weights, half a byte plus 2 / G written each; with a
+// division per weight the kernel was bound by its instructions (172 us for 117 M
+// bf16 weights, where their bytes take 46).  A lane owns eight consecutive weights
+// (one word of the packed row), sixteen lanes a block of 128; several blocks are in
+// flight per lane.
 #include "w4.cuh"
 
 namespace moe {
@@ -45,15 +50,42 @@ __device__ __forceinline__ uint16_t group_scale(uint32_t max_bits) {
     return __bfloat16_as_ushort(__float2bfloat16_rn(t));
 }
 
-__device__ __forceinline__ int quant(float w, float s) {
-    const float t = w / s;
-    float r = rintf(t);
-    if (fabsf(t - r) == 0.5f) {   // a tie of the rounded quotient
-        const float e = fmaf(-t, s, w);
-        if (e > 0.f) r = ceilf(t);
-        if (e < 0.f) r = floorf(t);
+// r = rint(t) of an approximate quotient t of w / s, put right and clamped
+__device__ __forceinline__ float settle(float w, float s, float r) {
+    const float d = fmaf(-r, s, w), a = fabsf(d), h = 0.5f * s;
+    if (a > h || (a == h && ((int)r & 1))) r += copysignf(1.f, d);
+    return fminf(fmaxf(r, -7.f), 7.f);
+}
+
+// A word of eight weights with scale s (finite, not 0), m their group's largest magnitude.
+__device__ __forceinline__ uint32_t quant8(const float (&v)[8], float s, float m) {
+    constexpr float kRound = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, ties to even
+    const float inv = __fdividef(1.f, s);
+    float r[8], worst = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        r[j] = fmaf(v[j], inv, kRound) - kRound;
+        worst = fmaxf(worst, fabsf(fmaf(-r[j], s, v[j])));
     }
-    return (int)fminf(fmaxf(r, -7.f), 7.f);
+    if (worst >= 0.5f * s) {   // a tie among the eight, or one that the quotient's error moved
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = settle(v[j], s, r[j]);
+    }
+    // tiny scales: the reciprocal flushes, and the scale's own rounding can take m / s past 7.5
+    if (s < 1e-36f || m > 7.5f * s) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[j] = settle(v[j], s, fabsf(v[j] / s) < 100.f ? rintf(v[j] / s) : copysignf(7.f, v[j]));
+    }
+    // weight 2 p + odd in bits 4 p + 16 odd: from the top, sixteen times what is there plus the next code,
+    // each with kRound's bits, whose sum over the places is taken off at the end
+    uint32_t word = 0, off = 0;
+#pragma unroll
+    for (int n = 7; n >= 0; --n) {
+        const int j = n < 4 ? 2 * n : 2 * (n - 4) + 1;
+        word = word * 16u + __float_as_uint(r[j] + (kRound + 8.f));
+        off = off * 16u + 0x4B400000u;
+    }
+    return word - off;
 }
 
 template <typename T, int G>
@@ -92,10 +124,7 @@ w4_quantize_kernel(const T* __restrict__ w, uint8_t* __restrict__ q, uint16_t* _
         const uint16_t sb = group_scale(m);
         const float s = __uint_as_float((uint32_t)sb << 16);
         const bool zero = m >= 0x7F800000u || s == 0.f;
-        uint32_t word = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)   // weight 2 p + odd in bits 4 p + 16 odd
-            word |= (uint32_t)((zero ? 0 : quant(v[i][j], s)) + 8) << (4 * (j >> 1) + 16 * (j & 1));
+        const uint32_t word = zero ? 0x88888888u : quant8(v[i], s, __uint_as_float(m));
         *reinterpret_cast<uint32_t*>(q + r * ((int64_t)nb * kW4BlockBytes) + b * kW4BlockBytes +
                                      4 * (4 * (l & 3) + (l >> 2))) = word;
         const int g = (b * kW4Block + 8 * l) / G;

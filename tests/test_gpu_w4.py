@@ -69,6 +69,30 @@ def test_quantisation_ties_and_near_ties():
         np.testing.assert_array_equal(q[0].cpu().numpy(), w4_ref.pack(qr))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantisation_of_extreme_magnitudes(dtype):
+    # from the largest to the smallest scales; the reference's bf16 is that of normal numbers, so
+    # groups whose scale is subnormal are held to the definition by their codes' range and value only
+    g = torch.Generator().manual_seed(9)
+    w = torch.randn(1, 40, 128, generator=g)
+    w = (w * torch.logspace(-36.5, 37.5, 40, dtype=torch.float64)[None, :, None].float()).to(dtype)
+    q, s, _, back = _quantize(w.cuda(), 128)
+    qr, sr = w4_ref.quantize(w[0].double().numpy(), 128)
+    np.testing.assert_array_equal(s[0].double().cpu().numpy(), sr)
+    np.testing.assert_array_equal(q[0].cpu().numpy(), w4_ref.pack(qr))
+    tiny = (torch.randn(1, 30, 64, generator=g).double() * torch.logspace(-45, -37.5, 30, dtype=torch.float64)[None, :, None]).to(dtype)
+    q, s, _, back = _quantize(tiny.cuda(), 64)
+    codes = q.cpu().numpy()
+    assert ((codes & 15) >= 1).all() and ((codes >> 4) >= 1).all()   # -7 .. 7
+    sv = s.double().cpu()[0, 0]
+    live = sv > 0
+    # the nearest of the representable multiples, or the largest of them
+    x = tiny[0].double() / sv.clamp(min=1e-300)[:, None]
+    want = torch.where(live[:, None], x, torch.zeros_like(x)).clamp(-7, 7)
+    got = torch.where(live[:, None], back[0].double().cpu() / sv.clamp(min=1e-300)[:, None], torch.zeros_like(x))
+    assert ((got - want).abs() <= 0.5).all() and (back[0].cpu()[~live] == 0).all()
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
 def test_non_finite_groups_stand_for_nan(bad):
     w = torch.randn(1, 3, 256)
