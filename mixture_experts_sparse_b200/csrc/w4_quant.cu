@@ -2,18 +2,19 @@
 // row, and back.
 //   scale = bf16(max |w| / 7),  q = rint(w / scale) in [-7, 7],  value = q scale.
 // Both are decided exactly, whatever a quotient in fp32 rounds to, so the result is
-// that of real arithmetic with ties to even.  For q: r = rint(w / s) from an
-// approximate quotient is at most one off, and the residual w - r s is exact in one
-// fma (r s has 12 bits, and what is left of w is a multiple of its last place and
-// below s); r is right iff |w - r s| < s / 2, and only the lanes' 8 weights for which
-// that fails, ties among them, take the long way.  A group of zeros has scale 0; a
-// group with an infinity or NaN has scale NaN and stands for NaN as a whole.
+// that of real arithmetic with ties to even.  Of fp32 weights: r = rint(w / s) from an
+// approximate quotient is at most one off, and the residual w - r s is exact in one fma
+// (r s has 12 bits, and what is left of w is a multiple of its last place and below
+// s); r is right iff |w - r s| < s / 2, and only lanes where that fails for one of
+// their eight weights, ties among them, take the long way.  bf16 weights leave room
+// between a tie and the next quotient, so rounding twice decides them.  A group of zeros
+// has scale 0; a group with an infinity or NaN has scale NaN and stands for NaN as a whole.
 //
-// Bound by HBM: one read of the weights, half a byte plus 2 / G written each; with a
-// division per weight the kernel was bound by its instructions (172 us for 117 M
-// bf16 weights, where their bytes take 46).  A lane owns eight consecutive weights
-// (one word of the packed row), sixteen lanes a block of 128; several blocks are in
-// flight per lane.
+// Bound by HBM in principle: one read of the weights, half a byte plus 2 / G written
+// each.  117 M bf16 weights take 74 us (46 at the copy rate) and 50 back; with a
+// division per weight the kernel was bound by its instructions and took 172.  A lane
+// owns eight consecutive weights (one word of the packed row), sixteen lanes a block of
+// 128; several blocks are in flight per lane.
 #include "w4.cuh"
 
 namespace moe {
@@ -21,27 +22,64 @@ namespace {
 
 constexpr int kQuantThreads = 256;
 constexpr int kQuantRows = kQuantThreads / 16;   // one row per 16 lanes
-constexpr int kQuantBlocks = 4;                  // consecutive 128-blocks per lane
+// Consecutive 128-blocks per lane: 64 bytes of weights in flight.  117 M bf16 weights there and
+// back take 130 / 111 / 120 / 111 us at 2 / 4 / 6 / 8 blocks, 5.2 M fp32 ones 15.7 / 19.1 at 2 / 4.
+template <typename T> constexpr int kBlocksOf = 8 / (int)sizeof(T);
 
+// eight weights as they lie in memory, their values and their largest magnitude's bits
+// (compared as integers: NaN above infinity above all numbers)
+template <typename T> struct Eight;
+template <> struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p));
+        b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+    template <int Lanes>
+    __device__ __forceinline__ uint32_t largest() const {   // over the Lanes lanes of a group
+        float v[8];
+        values(v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = Lanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    }
+};
+template <> struct Eight<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        v[0] = bf16lo(a.x); v[1] = bf16hi(a.x); v[2] = bf16lo(a.y); v[3] = bf16hi(a.y);
+        v[4] = bf16lo(a.z); v[5] = bf16hi(a.z); v[6] = bf16lo(a.w); v[7] = bf16hi(a.w);
+    }
+    template <int Lanes>
+    __device__ __forceinline__ uint32_t largest() const {
+        constexpr uint32_t kAbs = 0x7FFF7FFFu;
+        uint32_t m = __vmaxu2(__vmaxu2(a.x & kAbs, a.y & kAbs), __vmaxu2(a.z & kAbs, a.w & kAbs));
+        m = max(m & 0xFFFFu, m >> 16) << 16;
+#pragma unroll
+        for (int o = Lanes / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+    }
+};
+
+// max |w| / 7 to bf16, nearest even, of the real quotient.  Of a bf16 weight, whose eight
+// bits are never seven times the nine of a tie but at least 2^-12 away, the fp32 product
+// with 1 / 7 decides.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
-    v[0] = bf16lo(a.x); v[1] = bf16hi(a.x); v[2] = bf16lo(a.y); v[3] = bf16hi(a.y);
-    v[4] = bf16lo(a.z); v[5] = bf16hi(a.z); v[6] = bf16lo(a.w); v[7] = bf16hi(a.w);
-}
-
-// max |w| / 7 to bf16, nearest even, of the real quotient
 __device__ __forceinline__ uint16_t group_scale(uint32_t max_bits) {
     if (max_bits >= 0x7F800000u) return 0x7FC0u;
-    const float m = __uint_as_float(max_bits), t = m / 7.f;
+    const float m = __uint_as_float(max_bits);
+    if (sizeof(T) == 2 && m > 1e-30f) return __bfloat16_as_ushort(__float2bfloat16_rn(m * (1.f / 7.f)));
+    const float t = m / 7.f;
     const uint32_t b = __float_as_uint(t);
     if ((b & 0xFFFFu) == 0x8000u) {   // the fp32 quotient is a tie: the residual says where the real one lies
         const float r = fmaf(-t, 7.f, m);
@@ -58,18 +96,28 @@ __device__ __forceinline__ float settle(float w, float s, float r) {
 }
 
 // A word of eight weights with scale s (finite, not 0), m their group's largest magnitude.
+template <typename T>
 __device__ __forceinline__ uint32_t quant8(const float (&v)[8], float s, float m) {
     constexpr float kRound = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, ties to even
     const float inv = __fdividef(1.f, s);
-    float r[8], worst = 0.f;
+    float r[8];
+    if (sizeof(T) == 2) {
+        // w and s have eight bits each, so w / s is k + 1/2 or at least 2^-10 from it: to multiples
+        // of 2^-12 first (1.5 2^11), which puts a tie back in its place and moves nothing else across
+        constexpr float kSnap = 1.5f * 2048.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        r[j] = fmaf(v[j], inv, kRound) - kRound;
-        worst = fmaxf(worst, fabsf(fmaf(-r[j], s, v[j])));
-    }
-    if (worst >= 0.5f * s) {   // a tie among the eight, or one that the quotient's error moved
+        for (int j = 0; j < 8; ++j) r[j] = fmaf(v[j], inv, kSnap) - kSnap;
+    } else {
+        float worst = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[j] = settle(v[j], s, r[j]);
+        for (int j = 0; j < 8; ++j) {
+            r[j] = fmaf(v[j], inv, kRound) - kRound;
+            worst = fmaxf(worst, fabsf(fmaf(-r[j], s, v[j])));
+        }
+        if (worst >= 0.5f * s) {   // a tie among the eight, or one that the quotient's error moved
+#pragma unroll
+            for (int j = 0; j < 8; ++j) r[j] = settle(v[j], s, r[j]);
+        }
     }
     // tiny scales: the reciprocal flushes, and the scale's own rounding can take m / s past 7.5
     if (s < 1e-36f || m > 7.5f * s) {
@@ -88,10 +136,16 @@ __device__ __forceinline__ uint32_t quant8(const float (&v)[8], float s, float m
     return word - off;
 }
 
+// the matrix of row r; the 64-bit division costs as much as a block of weights
+__device__ __forceinline__ int64_t matrix_of(int64_t r, int64_t rows, int64_t all_rows) {
+    return all_rows <= 0xFFFFFFFFll ? (int64_t)((uint32_t)r / (uint32_t)rows) : r / rows;
+}
+
 template <typename T, int G>
 __global__ void __launch_bounds__(kQuantThreads)
 w4_quantize_kernel(const T* __restrict__ w, uint8_t* __restrict__ q, uint16_t* __restrict__ scale, int64_t all_rows,
                    int64_t rows, int k) {
+    constexpr int kQuantBlocks = kBlocksOf<T>;
     const int l = threadIdx.x & 15;
     const int64_t r = (int64_t)blockIdx.x * kQuantRows + (threadIdx.x >> 4);   // row of all matrices
     const int b0 = blockIdx.y * kQuantBlocks, nb = (k + kW4Block - 1) / kW4Block, ng = (k + G - 1) / G;
@@ -99,36 +153,29 @@ w4_quantize_kernel(const T* __restrict__ w, uint8_t* __restrict__ q, uint16_t* _
     pdl_launch();
     const bool live = r < all_rows;
     const T* src = w + r * k + 8 * l;
-    float v[kQuantBlocks][8];
+    Eight<T> raw[kQuantBlocks];
 #pragma unroll
     for (int i = 0; i < kQuantBlocks; ++i) {
         const int k0 = (b0 + i) * kW4Block;
-        if (live && k0 + 8 * l < k) {
-            load8(src + k0, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
+        if (live && k0 + 8 * l < k) raw[i].load(src + k0);
+        else raw[i].zero();
     }
-    const int64_t mat = r / rows, row = r - mat * rows;
+    const int64_t mat = matrix_of(r, rows, all_rows), row = r - mat * rows;
+    uint8_t* dst = q + (r * nb + b0) * kW4BlockBytes + 4 * (4 * (l & 3) + (l >> 2));
+    const int g0 = b0 * (kW4Block / G) + 8 * l / G;
+    uint16_t* sc = scale + (mat * ng + g0) * rows + row;
 #pragma unroll
     for (int i = 0; i < kQuantBlocks; ++i) {
-        // the group's largest magnitude, compared as bits: NaN above infinity above all numbers
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[i][j]) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int o = G / 16; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int b = b0 + i;
-        if (!live || b >= nb) continue;
-        const uint16_t sb = group_scale(m);
+        const uint32_t m = raw[i].template largest<G / 8>();
+        if (!live || b0 + i >= nb) continue;
+        const uint16_t sb = group_scale<T>(m);
         const float s = __uint_as_float((uint32_t)sb << 16);
-        const bool zero = m >= 0x7F800000u || s == 0.f;
-        const uint32_t word = zero ? 0x88888888u : quant8(v[i], s, __uint_as_float(m));
-        *reinterpret_cast<uint32_t*>(q + r * ((int64_t)nb * kW4BlockBytes) + b * kW4BlockBytes +
-                                     4 * (4 * (l & 3) + (l >> 2))) = word;
-        const int g = (b * kW4Block + 8 * l) / G;
-        if ((8 * l) % G == 0 && g < ng) scale[(mat * ng + g) * rows + row] = sb;
+        float v[8];
+        raw[i].values(v);
+        const uint32_t word =
+            m >= 0x7F800000u || s == 0.f ? 0x88888888u : quant8<T>(v, s, __uint_as_float(m));
+        *reinterpret_cast<uint32_t*>(dst + i * kW4BlockBytes) = word;
+        if ((8 * l) % G == 0 && g0 + i * (kW4Block / G) < ng) sc[(int64_t)i * (kW4Block / G) * rows] = sb;
     }
 }
 
@@ -149,13 +196,14 @@ template <typename T, int G>
 __global__ void __launch_bounds__(kQuantThreads)
 w4_dequantize_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__ scale, T* __restrict__ w,
                      int64_t all_rows, int64_t rows, int k) {
+    constexpr int kQuantBlocks = kBlocksOf<T>;
     const int l = threadIdx.x & 15;
     const int64_t r = (int64_t)blockIdx.x * kQuantRows + (threadIdx.x >> 4);
     const int b0 = blockIdx.y * kQuantBlocks, nb = (k + kW4Block - 1) / kW4Block, ng = (k + G - 1) / G;
     pdl_wait();
     pdl_launch();
     if (r >= all_rows) return;
-    const int64_t mat = r / rows, row = r - mat * rows;
+    const int64_t mat = matrix_of(r, rows, all_rows), row = r - mat * rows;
     uint32_t word[kQuantBlocks];
     uint16_t sb[kQuantBlocks];
 #pragma unroll
@@ -185,6 +233,7 @@ w4_dequantize_kernel(const uint8_t* __restrict__ q, const uint16_t* __restrict__
 template <typename T, int G>
 cudaError_t run(bool back, int64_t mats, int64_t rows, int64_t k, const void* w, uint8_t* q, uint16_t* scale,
                 cudaStream_t s) {
+    constexpr int kQuantBlocks = kBlocksOf<T>;
     const int64_t all = mats * rows;
     const dim3 grid((unsigned)((all + kQuantRows - 1) / kQuantRows),
                     (unsigned)((w4_blocks(k) + kQuantBlocks - 1) / kQuantBlocks));
