@@ -522,13 +522,13 @@ static BalanceLayout balance_layout(const moe_balance_config& c) {
         off += round_up(bytes, 256);
         return o;
     };
-    const size_t slots = (size_t)balance_slots(c.T, c.n_seqs), N = (size_t)c.n_experts, S = (size_t)c.n_seqs;
+    const size_t slots = (size_t)balance_slots(c.T, c.n_experts, c.n_seqs), N = (size_t)c.n_experts, S = (size_t)c.n_seqs;
     L.hdr = take(sizeof(WsHeader));
     L.slot_p = take(4 * slots * N);
     L.slot_c = take(4 * slots * N);
     L.slot_z = take(8 * slots);
     L.slot_n = take(4 * slots);
-    L.seq_term = take(8 * S);
+    L.seq_term = take(8 * S * ((N + 31) / 32));
     L.seq_z = take(8 * S);
     L.total = off;
     return L;

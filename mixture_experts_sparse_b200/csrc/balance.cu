@@ -17,7 +17,11 @@
 // Both passes are bound by HBM: the forward reads the logits and choices once,
 // the backward reads the logits again (the loss of the whole batch comes before
 // any gradient) and writes the gradient.  A row is held by L lanes, 4 C values
-// each, so the softmax needs log2 L shuffles and no shared memory.
+// each, so the softmax needs log2 L shuffles and no shared memory; with up to 16
+// values per lane the shuffles stay below a third of the instructions.  Rows are
+// loaded a batch ahead, whatever sequence they belong to.  262144 rows of 256 fp32
+// logits in 64 masked sequences, 8 choices each: forward 74 us (43 at the copy
+// rate), gradient 92 (83).
 //
 // Forward: a CTA owns a tile of consecutive tokens and walks the sequences that
 // cut it.  The share of (tile b, sequence s) goes to slot b + s of the
@@ -34,6 +38,7 @@ namespace {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalWarps = kBalThreads / 32;
+constexpr int kBalPerSm = 2;   // resident CTAs (with 3, which leaves 80 registers and spills: 201 us for 196)
 
 // e^z for z <= 0 to about an ulp: z log2 e in two parts, 2^hi in one MUFU and
 // the low part to first order.  Below -120 the result is 0 (fp32 underflow);
@@ -115,80 +120,229 @@ __device__ __forceinline__ void softmax_row(float (&v)[4 * C], float& lse) {
     for (int j = 0; j < 4 * C; ++j) v[j] *= inv;
 }
 
-__device__ __forceinline__ int64_t bound(int64_t v, int64_t T) { return v < 0 ? 0 : (v > T ? T : v); }
+// The rows of a warp's batch: U rows of 4 C values per lane, G = 32 / L rows side by side.
+template <int C> constexpr int kRowsAhead = C == 1 ? 4 : (C == 2 ? 2 : 1);
+
+template <typename T, int L, int C, bool VEC>
+struct Batch {
+    static constexpr int U = kRowsAhead<C>, G = 32 / L, kRows = U * G * kBalWarps;   // rows of the CTA
+    float v[U][4 * C];
+    int m[U];   // mask of a row in the tile, as loaded: a test here would wait for it
+    static __device__ __forceinline__ int row(int b, int u, int warp, int g) { return b + (u * kBalWarps + warp) * G + g; }
+    __device__ __forceinline__ void load(const BalanceArgs& a, int b, int t1, int warp, int l, int g) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int t = row(b, u, warp, g);
+            const bool in = t < t1;
+            m[u] = in && a.mask ? __ldg(a.mask + t) : 1;
+            load_row<T, L, C, VEC>(reinterpret_cast<const T*>(a.h) + (int64_t)t * a.ld, l, a.N, in, v[u]);
+        }
+    }
+};
 
 // first row of sequence s; without offsets the batch is one sequence
-__device__ __forceinline__ int64_t seq_at(const int32_t* seqs, int s, int64_t T) {
-    return seqs ? bound(__ldg(seqs + s), T) : (s == 0 ? 0 : T);
+__device__ __forceinline__ int seq_at(const BalanceArgs& a, int s) {
+    const int T = (int)a.T;
+    if (!a.seqs) return s == 0 ? 0 : T;
+    const int v = __ldg(a.seqs + s);
+    return v < 0 ? 0 : (v > T ? T : v);
 }
 
-// the last sequence that starts at or before row t (0 when none does)
-__device__ __forceinline__ int first_seq(const int32_t* seqs, int S, int64_t t, int64_t T) {
-    int lo = 0, hi = S;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (seq_at(seqs, mid, T) <= t) lo = mid;
-        else hi = mid;
+// The last sequence that starts at or before row t (0 when none does), by a whole warp:
+// 32 bounds at a time, so two dependent loads for up to 1024 sequences.
+__device__ __forceinline__ int first_seq(const BalanceArgs& a, int t, int lane) {
+    int lo = 0, n = a.S;   // it is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int s = lo + lane * step;
+        const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && seq_at(a, s) <= t);
+        const int last = le ? 31 - __clz(le) : 0;
+        n = min(step, n - last * step);
+        lo += last * step;
     }
     return lo;
 }
 
-template <typename T, int L, int C, bool VEC>
-__global__ void __launch_bounds__(kBalThreads)
-balance_tile_kernel(const BalanceArgs a) {
-    constexpr int G = 32 / L;              // rows a warp holds at once
-    constexpr int U = C == 1 ? 4 : 2;      // row loads in flight per lane
-    __shared__ float s_p[kBalWarps][4 * C * L];
-    __shared__ int s_cnt[kBalWarps][4 * C * L];
-    __shared__ double s_z[kBalWarps];
-    __shared__ int s_n[kBalWarps];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L, g = lane / L;
-    const int N = a.N;
-    const T* h = reinterpret_cast<const T*>(a.h);
-    for (int j = lane; j < 4 * C * L; j += 32) s_cnt[warp][j] = 0;
-    pdl_wait();
-    pdl_launch();
-    const int64_t t0 = (int64_t)blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
-    for (int s = first_seq(a.seqs, a.S, t0, a.T); s < a.S; ++s) {
-        const int64_t q0 = seq_at(a.seqs, s, a.T);
-        if (q0 >= t1) break;
-        const int64_t p0 = max(t0, q0), p1 = min(t1, seq_at(a.seqs, s + 1, a.T));
-        if (p0 >= p1) continue;   // an empty sequence, or one that ends before the tile
-        float acc[4 * C];
-#pragma unroll
-        for (int j = 0; j < 4 * C; ++j) acc[j] = 0.f;
+// ---- sums over the tiles ------------------------------------------------------
+
+template <int Ways> struct SumShared {
+    double p[Ways][32];
+    int c[Ways][32];
+    double z;
+    int n;
+};
+
+// Unit (sequence s, 32 experts): the shares of the sequence's tiles, Ways warps taking every
+// Ways-th tile and warp 0 adding theirs in order.  Another warp adds the token counts and lse^2.
+template <int Ways>
+__device__ __forceinline__ void sum_unit(const BalanceArgs& a, int unit, SumShared<Ways>& sh) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, N = a.N, chunks = (N + 31) / 32;
+    const int s = unit / chunks, e = (unit - s * chunks) * 32 + lane;
+    const int q0 = seq_at(a, s), q1 = seq_at(a, s + 1);
+    const int b0 = q0 / a.tile, b1 = q1 > q0 ? (q1 - 1) / a.tile + 1 : b0;
+    double p = 0.0;
+    int c = 0;
+    if (e < N) {
+#pragma unroll 8
+        for (int b = b0 + warp; b < b1; b += Ways) {
+            p += (double)__ldcg(a.slot_p + (int64_t)(b + s) * N + e);
+            c += __ldcg(a.slot_c + (int64_t)(b + s) * N + e);
+        }
+    }
+    sh.p[warp][lane] = p;
+    sh.c[warp][lane] = c;
+    if (warp == Ways - 1) {
         double z = 0.0;
         int n = 0;
-        for (int64_t b = p0 + warp * G; b < p1; b += (int64_t)kBalWarps * G * U) {
-            float v[U][4 * C];
-            bool ok[U];
+#pragma unroll 4
+        for (int b = b0 + lane; b < b1; b += 32) {
+            n += __ldcg(a.slot_n + b + s);
+            z += __ldcg(a.slot_z + b + s);
+        }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t t = b + (int64_t)u * kBalWarps * G + g;
-                ok[u] = t < p1;
-                load_row<T, L, C, VEC>(h + t * a.ld, l, N, ok[u], v[u]);
-                ok[u] = ok[u] && (!a.mask || __ldg(a.mask + t) != 0);
-            }
+        for (int o = 16; o > 0; o >>= 1) {
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+        }
+        if (lane == 0) {
+            sh.n = n;
+            sh.z = z;
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int n = sh.n;
+        p = 0.0;
+        c = 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float lse;
-                softmax_row<L, C>(v[u], lse);
-                if (ok[u]) {
+        for (int w = 0; w < Ways; ++w) {
+            p += sh.p[w][lane];
+            c += sh.c[w][lane];
+        }
+        double term = 0.0;
+        if (e < N) {
+            const double P = n > 0 ? p / (double)n : 0.0;
+            if (a.P) a.P[(int64_t)s * N + e] = (float)P;
+            a.counts[(int64_t)s * N + e] = c;
+            term = n > 0 ? P * (double)c / ((double)a.k * (double)n) : 0.0;
+        }
 #pragma unroll
-                    for (int j = 0; j < 4 * C; ++j) acc[j] += v[u][j];
-                    z += (double)lse * (double)lse;
-                    ++n;
-                }
+        for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
+        if (lane == 0) {
+            a.seq_term[unit] = term;
+            if (unit == s * chunks) {
+                a.seq_z[s] = sh.z;
+                a.tokens[s] = n;
             }
         }
-        for (int64_t t = p0 + tid; t < p1; t += kBalThreads) {
-            if (a.mask && __ldg(a.mask + t) == 0) continue;
-            for (int r = 0; r < a.k; ++r) {
-                const int e = __ldg(a.idx + t * a.k + r);
-                if ((unsigned)e < (unsigned)N) atomicAdd(&s_cnt[warp][e], 1);
-            }
-        }
-        // the warp's rows, then the warps in order
+    }
+    __syncthreads();   // before the next unit's shares
+}
+
+// the units' terms in order, by one warp that sees them all
+__device__ __forceinline__ void sum_losses(const BalanceArgs& a, int lane) {
+    const int units = a.S * ((a.N + 31) / 32);
+    double t = 0.0, z = 0.0;
+    int n = 0, used = 0;
+#pragma unroll 4
+    for (int u = lane; u < units; u += 32) t += __ldcg(a.seq_term + u);
+#pragma unroll 4
+    for (int s = lane; s < a.S; s += 32) {
+        z += __ldcg(a.seq_z + s);
+        const int ns = __ldcg(a.tokens + s);
+        n += ns;
+        used += ns > 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        t += __shfl_xor_sync(0xffffffffu, t, o);
+        z += __shfl_xor_sync(0xffffffffu, z, o);
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+        used += __shfl_xor_sync(0xffffffffu, used, o);
+    }
+    if (lane == 0) {
+        a.loss[0] = (float)((double)a.alpha * a.N * t / (used > 0 ? used : 1));
+        a.loss[1] = (float)((double)a.z_coef * z / (n > 0 ? n : 1));
+        a.tokens[a.S] = n;
+        a.tokens[a.S + 1] = used;
+    }
+}
+
+// Units over the grid; the CTA that finishes last adds their terms.
+constexpr int kBalSumWays = 16;
+
+__global__ void __launch_bounds__(32 * kBalSumWays)
+balance_sum_kernel(const BalanceArgs a) {
+    __shared__ SumShared<kBalSumWays> sh;
+    const int lane = threadIdx.x & 31, units = a.S * ((a.N + 31) / 32);
+    pdl_wait();
+    pdl_launch();
+    for (int u = blockIdx.x; u < units; u += gridDim.x) sum_unit<kBalSumWays>(a, u, sh);
+    if (threadIdx.x >= 32) return;
+    int last = 1;
+    if (lane == 0 && gridDim.x > 1) {
+        __threadfence();
+        last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+        if (last) *a.ticket = 0;
+    }
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    __threadfence();
+    sum_losses(a, lane);
+}
+
+// ---- one pass over the tokens -------------------------------------------------
+
+template <int W> struct TileShared {   // W experts, padded
+    float p[kBalWarps][W];
+    int cnt[kBalWarps][W];
+    double z[kBalWarps];
+    int n[kBalWarps];
+};
+
+// FUSED: the tile that finishes last also sums, without a second launch
+template <typename T, int L, int C, bool VEC, bool FUSED>
+__global__ void __launch_bounds__(kBalThreads, kBalPerSm)
+balance_tile_kernel(const BalanceArgs a) {
+    using B = Batch<T, L, C, VEC>;
+    constexpr int U = B::U;
+    __shared__ TileShared<4 * C * L> sh;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L, g = lane / L;
+    const int N = a.N;
+    for (int j = lane; j < 4 * C * L; j += 32) sh.cnt[warp][j] = 0;
+    pdl_wait();
+    if (!FUSED) pdl_launch();
+    const int t0 = (int)blockIdx.x * a.tile, t1 = (int)min(a.T, (int64_t)t0 + a.tile);
+    B next;
+    next.load(a, t0, t1, warp, l, g);
+    int s = first_seq(a, t0, lane), q0 = seq_at(a, s), q1 = seq_at(a, s + 1);
+    float acc[4 * C];
+    double z = 0.0;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < 4 * C; ++j) acc[j] = 0.f;
+
+    // Choice j of the batch at b is that of row b + j / k; the first E per thread are loaded a batch
+    // ahead (a sequence's choices all at its start, each behind the test of its mask, took a third of
+    // the kernel's time; the shared-memory atomics themselves are free).
+    constexpr int E = C == 4 ? 2 : 4;
+    const uint32_t inv = 0xFFFFFFFFu / (uint32_t)a.k + 1u;   // j < 2^14: the quotient by k is one product
+    auto row_of = [&](int b, int j) { return b + (a.k == 1 ? j : (int)__umulhi((uint32_t)j, inv)); };
+    auto choice = [&](int b, int j, int& m) {
+        const int t = row_of(b, j);
+        const bool in = j < B::kRows * a.k && t < t1;
+        m = in && a.mask ? __ldg(a.mask + t) : 1;
+        return in ? __ldg(a.idx + (int64_t)b * a.k + j) : -1;
+    };
+    auto count = [&](int b, int j, int e, int m) {
+        const int t = row_of(b, j);
+        if ((unsigned)e < (unsigned)N && m != 0 && t >= q0 && t < q1) atomicAdd(&sh.cnt[warp][e], 1);
+    };
+    int ne[E], nm[E];
+#pragma unroll
+    for (int i = 0; i < E; ++i) ne[i] = choice(t0, tid + i * kBalThreads, nm[i]);
+    // the share of sequence s: the warp's rows, then the warps in order
+    auto flush = [&]() {
+        if (max(t0, q0) >= min(t1, q1)) return;   // no row of it in the tile
 #pragma unroll
         for (int o = L; o < 32; o <<= 1) {
 #pragma unroll
@@ -200,11 +354,11 @@ balance_tile_kernel(const BalanceArgs a) {
 #pragma unroll
             for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s_p[warp][col_of<L, C, VEC>(l, c, i)] = acc[4 * c + i];
+                for (int i = 0; i < 4; ++i) sh.p[warp][col_of<L, C, VEC>(l, c, i)] = acc[4 * c + i];
         }
         if (lane == 0) {
-            s_z[warp] = z;
-            s_n[warp] = n;
+            sh.z[warp] = z;
+            sh.n[warp] = n;
         }
         __syncthreads();
         const int64_t slot = (int64_t)blockIdx.x + s;
@@ -213,199 +367,158 @@ balance_tile_kernel(const BalanceArgs a) {
             int c = 0;
 #pragma unroll
             for (int w = 0; w < kBalWarps; ++w) {
-                p += (double)s_p[w][e];
-                c += s_cnt[w][e];
-                s_cnt[w][e] = 0;
+                p += (double)sh.p[w][e];
+                c += sh.cnt[w][e];
+                sh.cnt[w][e] = 0;
             }
             a.slot_p[slot * N + e] = (float)p;
             a.slot_c[slot * N + e] = c;
         }
-        if (tid == 0) {
-            double zs = 0.0;
-            int ns = 0;
-            for (int w = 0; w < kBalWarps; ++w) {
-                zs += s_z[w];
-                ns += s_n[w];
-            }
-            a.slot_z[slot] = zs;
-            a.slot_n[slot] = ns;
-        }
-        __syncthreads();
-    }
-}
-
-// One CTA per sequence (grid-stride): its shares in tile order, then the CTA that
-// finishes last adds the sequences' terms in sequence order.
-constexpr int kBalSumThreads = 512;
-
-__global__ void __launch_bounds__(kBalSumThreads)
-balance_sum_kernel(const BalanceArgs a) {
-    __shared__ double s_p[kBalSumThreads];
-    __shared__ int s_c[kBalSumThreads];
-    __shared__ double s_red[kBalSumThreads / 32];
-    __shared__ int s_n[kBalSumThreads / 32];
-    __shared__ int s_last;
-    const int tid = threadIdx.x, N = a.N;
-    const int ways = kBalSumThreads / N;   // threads per expert (N <= 512)
-    const int e = tid % N, way = tid / N;
-    pdl_wait();
-    pdl_launch();
-    for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
-        const int64_t q0 = seq_at(a.seqs, s, a.T), q1 = seq_at(a.seqs, s + 1, a.T);
-        const int64_t b0 = q0 / a.tile, b1 = q1 > q0 ? (q1 - 1) / a.tile + 1 : b0;
-        double p = 0.0;
-        int c = 0;
-        if (way < ways) {
-#pragma unroll 8
-            for (int64_t b = b0 + way; b < b1; b += ways) {
-                p += (double)a.slot_p[(b + s) * N + e];
-                c += a.slot_c[(b + s) * N + e];
-            }
-        }
-        s_p[tid] = p;
-        s_c[tid] = c;
-        __syncthreads();
-        int n = 0;
-        double z = 0.0;
-        for (int64_t b = b0 + tid; b < b1; b += kBalSumThreads) {
-            n += a.slot_n[b + s];
-            z += a.slot_z[b + s];
-        }
-        // n and z over the block, in fixed order
+        if (warp == kBalWarps - 1) {
+            double zs = lane < kBalWarps ? sh.z[lane] : 0.0;
+            int ns = lane < kBalWarps ? sh.n[lane] : 0;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-        }
-        if ((tid & 31) == 0) {
-            s_n[tid >> 5] = n;
-            s_red[tid >> 5] = z;
+            for (int o = kBalWarps / 2; o > 0; o >>= 1) {
+                zs += __shfl_xor_sync(0xffffffffu, zs, o);
+                ns += __shfl_xor_sync(0xffffffffu, ns, o);
+            }
+            if (lane == 0) {
+                a.slot_z[slot] = zs;
+                a.slot_n[slot] = ns;
+            }
         }
         __syncthreads();
-        n = 0;
+#pragma unroll
+        for (int j = 0; j < 4 * C; ++j) acc[j] = 0.f;
         z = 0.0;
-        for (int w = 0; w < kBalSumThreads / 32; ++w) {
-            n += s_n[w];
-            z += s_red[w];
+        n = 0;
+    };
+
+#pragma unroll 1
+    for (int b = t0; b < t1; b += B::kRows) {
+        B cur = next;
+        int e[E], em[E];
+        next.load(a, b + B::kRows, t1, warp, l, g);
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            e[i] = ne[i];
+            em[i] = nm[i];
+            ne[i] = choice(b + B::kRows, tid + i * kBalThreads, nm[i]);
         }
-        double term = 0.0;
-        if (tid < N) {
-            for (int w = 1; w < ways; ++w) {
-                p += s_p[tid + w * N];
-                c += s_c[tid + w * N];
+        float lse[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) softmax_row<L, C>(cur.v[u], lse[u]);
+        for (;;) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = B::row(b, u, warp, g);
+                if (cur.m[u] != 0 && t >= q0 && t < min(q1, t1)) {
+#pragma unroll
+                    for (int j = 0; j < 4 * C; ++j) acc[j] += cur.v[u][j];
+                    z += (double)lse[u] * (double)lse[u];
+                    ++n;
+                }
             }
-            const double P = n > 0 ? p / (double)n : 0.0;
-            if (a.P) a.P[(int64_t)s * N + tid] = (float)P;
-            a.counts[(int64_t)s * N + tid] = c;
-            term = n > 0 ? P * (double)c / ((double)a.k * (double)n) : 0.0;
-        }
-        __syncthreads();
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) term += __shfl_xor_sync(0xffffffffu, term, o);
-        if ((tid & 31) == 0) s_red[tid >> 5] = term;
-        __syncthreads();
-        if (tid == 0) {
-            double t = 0.0;
-            for (int w = 0; w < kBalSumThreads / 32; ++w) t += s_red[w];
-            a.seq_term[s] = t;
-            a.seq_z[s] = z;
-            a.tokens[s] = n;
+            for (int i = 0; i < E; ++i) count(b, tid + i * kBalThreads, e[i], em[i]);
+#pragma unroll 4
+            for (int j = tid + E * kBalThreads; j < B::kRows * a.k; j += kBalThreads) {
+                int m;
+                const int x = choice(b, j, m);
+                count(b, j, x, m);
+            }
+            if (q1 >= min(b + B::kRows, t1) || s + 1 >= a.S) break;
+            flush();
+            ++s;
+            q0 = q1;
+            q1 = seq_at(a, s + 1);
         }
-        __syncthreads();
     }
-    if (tid == 0) {
+    flush();
+
+    if constexpr (FUSED) {
+        __shared__ SumShared<kBalWarps> sum;
+        __shared__ int s_last;
+        int last = 1;
+        if (gridDim.x > 1) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
+                if (s_last) *a.ticket = 0;
+            }
+            __syncthreads();
+            last = s_last;
+        }
+        pdl_launch();
+        if (!last) return;
         __threadfence();
-        s_last = atomicAdd(a.ticket, 1) == (int)gridDim.x - 1;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    if (tid < 32) {
-        double t = 0.0, z = 0.0;
-        int n = 0, used = 0;
-        for (int s = tid; s < a.S; s += 32) {
-            t += __ldcg(a.seq_term + s);
-            z += __ldcg(a.seq_z + s);
-            const int ns = __ldcg(a.tokens + s);
-            n += ns;
-            used += ns > 0;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            t += __shfl_xor_sync(0xffffffffu, t, o);
-            z += __shfl_xor_sync(0xffffffffu, z, o);
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-            used += __shfl_xor_sync(0xffffffffu, used, o);
-        }
-        if (tid == 0) {
-            a.loss[0] = (float)((double)a.alpha * N * t / (used > 0 ? used : 1));
-            a.loss[1] = (float)((double)a.z_coef * z / (n > 0 ? n : 1));
-            a.tokens[a.S] = n;
-            a.tokens[a.S + 1] = used;
-            *a.ticket = 0;
-        }
+        __syncthreads();
+        for (int u = 0, units = a.S * ((N + 31) / 32); u < units; ++u) sum_unit<kBalWarps>(a, u, sum);
+        if (warp == 0) sum_losses(a, lane);
     }
 }
 
 template <typename T, int L, int C, bool VEC>
-__global__ void __launch_bounds__(kBalThreads)
+__global__ void __launch_bounds__(kBalThreads, kBalPerSm)
 balance_grad_kernel(const BalanceArgs a) {
-    constexpr int G = 32 / L;
-    constexpr int U = C == 1 ? 4 : 2;
+    using B = Batch<T, L, C, VEC>;
+    constexpr int U = B::U;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L, g = lane / L;
     const int N = a.N;
-    const T* h = reinterpret_cast<const T*>(a.h);
     T* dh = reinterpret_cast<T*>(a.dh);
     pdl_wait();
     pdl_launch();
-    const int64_t t0 = (int64_t)blockIdx.x * a.tile, t1 = min(a.T, t0 + a.tile);
+    const int t0 = (int)blockIdx.x * a.tile, t1 = (int)min(a.T, (int64_t)t0 + a.tile);
+    B next;
+    next.load(a, t0, t1, warp, l, g);
     const int total = __ldg(a.tokens + a.S), used = __ldg(a.tokens + a.S + 1);
     const float g0 = a.dloss ? __ldg(a.dloss) : 1.f, g1 = a.dloss ? __ldg(a.dloss + 1) : 1.f;
-    const float zc = (float)((double)g1 * 2.0 * a.z_coef / (total > 0 ? total : 1));
-    for (int s = first_seq(a.seqs, a.S, t0, a.T); s < a.S; ++s) {
-        const int64_t q0 = seq_at(a.seqs, s, a.T);
-        if (q0 >= t1) break;
-        const int64_t p0 = max(t0, q0), p1 = min(t1, seq_at(a.seqs, s + 1, a.T));
-        if (p0 >= p1) continue;
+    int s = first_seq(a, t0, lane), q0 = seq_at(a, s), q1 = seq_at(a, s + 1);
+    const float zc = 2.f * a.z_coef * g1 / (float)max(total, 1);
+    float av[4 * C];
+    // a_s at this lane's columns; the two quotients apart, so that neither leaves fp32's range early
+    auto coefs = [&]() {
         const int ns = __ldg(a.tokens + s);
-        const double w = ns > 0 && used > 0 ? (double)g0 * a.alpha * N / ((double)used * ns) / ((double)a.k * ns) : 0.0;
-        float av[4 * C];
+        int c[4 * C];
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+        for (int j = 0; j < 4 * C; ++j) {
+            const int e = col_of<L, C, VEC>(l, j / 4, j % 4);
+            c[j] = e < N ? __ldg(a.counts + (int64_t)s * N + e) : 0;
+        }
+        const bool any = ns > 0 && used > 0;
+        const float w = any ? g0 * a.alpha * (float)N / ((float)used * (float)ns) : 0.f;
+        const float f = any ? 1.f / ((float)a.k * (float)ns) : 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = col_of<L, C, VEC>(l, c, i);
-                av[4 * c + i] = e < N ? (float)(w * (double)__ldg(a.counts + (int64_t)s * N + e)) : 0.f;
-            }
-        for (int64_t b = p0 + warp * G; b < p1; b += (int64_t)kBalWarps * G * U) {
-            float v[U][4 * C];
-            bool in[U], ok[U];
+        for (int j = 0; j < 4 * C; ++j) av[j] = w * ((float)c[j] * f);
+    };
+    coefs();
+#pragma unroll 1
+    for (int b = t0; b < t1; b += B::kRows) {
+        B cur = next;
+        next.load(a, b + B::kRows, t1, warp, l, g);
+        float lse[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) softmax_row<L, C>(cur.v[u], lse[u]);
+        for (;;) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t t = b + (int64_t)u * kBalWarps * G + g;
-                in[u] = t < p1;
-                load_row<T, L, C, VEC>(h + t * a.ld, l, N, in[u], v[u]);
-                ok[u] = in[u] && (!a.mask || __ldg(a.mask + t) != 0);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int64_t t = b + (int64_t)u * kBalWarps * G + g;
-                float lse;
-                softmax_row<L, C>(v[u], lse);
+                const int t = B::row(b, u, warp, g);
                 float dot = 0.f;
 #pragma unroll
-                for (int j = 0; j < 4 * C; ++j) dot = fmaf(v[u][j], av[j], dot);
+                for (int j = 0; j < 4 * C; ++j) dot = fmaf(cur.v[u][j], av[j], dot);
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-                const float shift = fmaf(zc, lse, -dot);
-                if (!in[u] || (!ok[u] && a.accumulate)) continue;
-                T* row = dh + t * a.dld;
+                const float shift = fmaf(zc, lse[u], -dot);
+                const bool ok = cur.m[u] != 0;
+                if (t < q0 || t >= min(q1, t1) || (!ok && a.accumulate)) continue;
+                T* row = dh + (int64_t)t * a.dld;
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     float d[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        d[i] = ok[u] ? v[u][4 * c + i] * (av[4 * c + i] + shift) : 0.f;
+                        d[i] = ok ? cur.v[u][4 * c + i] * (av[4 * c + i] + shift) : 0.f;
                     if (VEC) {
                         if (col_of<L, C, VEC>(l, c, 0) < N) {
                             auto* q = reinterpret_cast<typename Quad<T>::type*>(row) + l + L * c;
@@ -426,66 +539,85 @@ balance_grad_kernel(const BalanceArgs a) {
                     }
                 }
             }
+            if (q1 >= min(b + B::kRows, t1) || s + 1 >= a.S) break;
+            ++s;
+            q0 = q1;
+            q1 = seq_at(a, s + 1);
+            coefs();
         }
     }
 }
 
+enum class BalPass { kForward, kFused, kGrad };
+
 template <typename T, int L, int C, bool VEC>
-cudaError_t launch_shape(const BalanceArgs& a, bool grad, unsigned tiles, cudaStream_t s) {
-    return grad ? launch_k(balance_grad_kernel<T, L, C, VEC>, dim3(tiles), dim3(kBalThreads), 0, s, 1, a)
-                : launch_k(balance_tile_kernel<T, L, C, VEC>, dim3(tiles), dim3(kBalThreads), 0, s, 1, a);
+cudaError_t launch_shape(const BalanceArgs& a, BalPass pass, unsigned tiles, cudaStream_t s) {
+    if (pass == BalPass::kGrad)
+        return launch_k(balance_grad_kernel<T, L, C, VEC>, dim3(tiles), dim3(kBalThreads), 0, s, 1, a);
+    return pass == BalPass::kFused
+               ? launch_k(balance_tile_kernel<T, L, C, VEC, true>, dim3(tiles), dim3(kBalThreads), 0, s, 1, a)
+               : launch_k(balance_tile_kernel<T, L, C, VEC, false>, dim3(tiles), dim3(kBalThreads), 0, s, 1, a);
 }
 
 template <typename T, bool VEC>
-cudaError_t launch_typed(const BalanceArgs& a, bool grad, unsigned tiles, cudaStream_t s) {
-    if (a.N <= 4) return launch_shape<T, 1, 1, VEC>(a, grad, tiles, s);
-    if (a.N <= 8) return launch_shape<T, 2, 1, VEC>(a, grad, tiles, s);
-    if (a.N <= 16) return launch_shape<T, 4, 1, VEC>(a, grad, tiles, s);
-    if (a.N <= 32) return launch_shape<T, 8, 1, VEC>(a, grad, tiles, s);
-    if (a.N <= 64) return launch_shape<T, 16, 1, VEC>(a, grad, tiles, s);
-    if (a.N <= 128) return launch_shape<T, 32, 1, VEC>(a, grad, tiles, s);
-    if (a.N <= 256) return launch_shape<T, 32, 2, VEC>(a, grad, tiles, s);
-    return launch_shape<T, 32, 4, VEC>(a, grad, tiles, s);
+cudaError_t launch_typed(const BalanceArgs& a, BalPass pass, unsigned tiles, cudaStream_t s) {
+    if (a.N <= 4) return launch_shape<T, 1, 1, VEC>(a, pass, tiles, s);
+    if (a.N <= 8) return launch_shape<T, 2, 1, VEC>(a, pass, tiles, s);
+    if (a.N <= 16) return launch_shape<T, 4, 1, VEC>(a, pass, tiles, s);
+    if (a.N <= 32) return launch_shape<T, 4, 2, VEC>(a, pass, tiles, s);
+    if (a.N <= 64) return launch_shape<T, 4, 4, VEC>(a, pass, tiles, s);
+    if (a.N <= 128) return launch_shape<T, 8, 4, VEC>(a, pass, tiles, s);
+    if (a.N <= 256) return launch_shape<T, 16, 4, VEC>(a, pass, tiles, s);
+    return launch_shape<T, 32, 4, VEC>(a, pass, tiles, s);
 }
 
-cudaError_t launch_any(const BalanceArgs& a, bool grad, unsigned tiles, cudaStream_t s) {
+cudaError_t launch_any(const BalanceArgs& a, BalPass pass, unsigned tiles, cudaStream_t s) {
     // four columns per access need aligned rows and no ragged last quad
-    const bool vec = a.N % 4 == 0 && a.ld % 4 == 0 && (!grad || a.dld % 4 == 0);
+    const bool vec = a.N % 4 == 0 && a.ld % 4 == 0 && (pass != BalPass::kGrad || a.dld % 4 == 0);
     if (a.dtype == MOE_BF16)
-        return vec ? launch_typed<__nv_bfloat16, true>(a, grad, tiles, s)
-                   : launch_typed<__nv_bfloat16, false>(a, grad, tiles, s);
-    return vec ? launch_typed<float, true>(a, grad, tiles, s) : launch_typed<float, false>(a, grad, tiles, s);
+        return vec ? launch_typed<__nv_bfloat16, true>(a, pass, tiles, s)
+                   : launch_typed<__nv_bfloat16, false>(a, pass, tiles, s);
+    return vec ? launch_typed<float, true>(a, pass, tiles, s) : launch_typed<float, false>(a, pass, tiles, s);
+}
+
+// rows of one batch of a CTA (Batch::kRows): 4096 values of rows padded to a power of two
+int batch_rows(int N) {
+    int np = 4;
+    while (np < N) np *= 2;
+    return 4096 / np;
 }
 
 }  // namespace
 
-// Tokens per CTA of the forward: 296 tiles (two per SM) while a tile stays
-// between 64 tokens and the 4096 over which a lane may sum p in fp32.
-int balance_tile(int64_t T) {
-    int64_t t = (T + 295) / 296;
-    return (int)(t < 64 ? 64 : (t > 4096 ? 4096 : t));
+// Tokens per CTA of the forward: kBalPerSm tiles per SM while a tile stays between one
+// batch and the 4096 over which a lane may sum p in fp32.
+int balance_tile(int64_t T, int N) {
+    const int64_t t = (T + 148 * kBalPerSm - 1) / (148 * kBalPerSm), lo = batch_rows(N);
+    return (int)(t < lo ? lo : (t > 4096 ? 4096 : t));
 }
-int64_t balance_slots(int64_t T, int S) {
-    const int64_t tile = balance_tile(T);
+int64_t balance_slots(int64_t T, int N, int S) {
+    const int64_t tile = balance_tile(T, N);
     return (T + tile - 1) / tile + S;
 }
 
 cudaError_t launch_balance_loss(BalanceArgs a, cudaStream_t s) {
-    a.tile = balance_tile(a.T);
-    const unsigned tiles = (unsigned)((a.T + a.tile - 1) / a.tile);
+    a.tile = balance_tile(a.T, a.N);
+    const int64_t tiles = (a.T + a.tile - 1) / a.tile, units = (int64_t)a.S * ((a.N + 31) / 32);
+    // few tiles and units: one CTA adds them sooner than a second launch would (512 rows of 8: 6.4 us for 9.2)
+    const bool fused = tiles > 0 && tiles <= 64 && units <= 4;
     if (tiles > 0) {
-        const cudaError_t err = launch_any(a, false, tiles, s);
-        if (err != cudaSuccess) return err;
+        const cudaError_t err = launch_any(a, fused ? BalPass::kFused : BalPass::kForward, (unsigned)tiles, s);
+        if (err != cudaSuccess || fused) return err;
     }
-    const unsigned grid = (unsigned)(a.S < 1024 ? a.S : 1024);
-    return launch_k(balance_sum_kernel, dim3(grid), dim3(kBalSumThreads), 0, s, 1, a);
+    return launch_k(balance_sum_kernel, dim3((unsigned)(units < 1024 ? units : 1024)), dim3(32 * kBalSumWays), 0, s, 1, a);
 }
 
 cudaError_t launch_balance_grad(BalanceArgs a, cudaStream_t s) {
     if (a.T <= 0) return cudaSuccess;
-    int64_t t = (a.T + 148 * 8 - 1) / (148 * 8);
-    a.tile = (int)(t < 64 ? 64 : t);
-    return launch_any(a, true, (unsigned)((a.T + a.tile - 1) / a.tile), s);
+    // a row per lane group at least, which spreads a small batch over the SMs
+    const int64_t t = (a.T + 148 * 8 - 1) / (148 * 8), lo = a.N <= 16 ? batch_rows(a.N) / 4 : batch_rows(a.N);
+    a.tile = (int)(t < lo ? lo : t);
+    return launch_any(a, BalPass::kGrad, (unsigned)((a.T + a.tile - 1) / a.tile), s);
 }
 
 }  // namespace moe

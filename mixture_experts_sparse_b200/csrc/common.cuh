@@ -262,11 +262,11 @@ struct BalanceArgs {
     float alpha; float z_coef;
     float* loss; int32_t* counts; float* P; int32_t* tokens;
     float* slot_p; int32_t* slot_c; double* slot_z; int32_t* slot_n;   // [balance_slots(T, S)](, N)
-    double* seq_term; double* seq_z;          // [S]
+    double* seq_term; double* seq_z;          // [S, ceil(N / 32)], [S]
     int32_t* ticket;
     const float* dloss; void* dh; int64_t dld; bool accumulate;
 };
-int64_t balance_slots(int64_t T, int S);
+int64_t balance_slots(int64_t T, int N, int S);
 cudaError_t launch_balance_loss(BalanceArgs a, cudaStream_t s);
 cudaError_t launch_balance_grad(BalanceArgs a, cudaStream_t s);
 
