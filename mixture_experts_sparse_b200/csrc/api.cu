@@ -749,7 +749,7 @@ static int32_t w4_check(int64_t mats, int64_t rows, int64_t k, int32_t group, in
                         const void* q, const void* scale) {
     if (mats < 0 || rows < 0 || k < 1) return MOE_ERR_INVALID_ARG;
     if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
-    if (!w4_group_ok(group) || k % 16 != 0 || k > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (!w4_group_ok(group) || k % 16 != 0 || k > (1 << 23)) return MOE_ERR_UNSUPPORTED;
     if (mats >= (1LL << 31) || rows >= (1LL << 31) || (mats > 0 && rows > (1LL << 34) / mats)) return MOE_ERR_UNSUPPORTED;
     if (mats > 0 && rows > 0 && (!req(w) || !req(q) || !req(scale))) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
@@ -781,7 +781,10 @@ static int32_t w4_check_weights(const moe_config* cfg, const W4Weights& w) {
     if (cfg->dtype != MOE_BF16 || !w4_group_ok(w.group)) return MOE_ERR_UNSUPPORTED;
     // weight rows are 32-bit tensor-map coordinates
     const int64_t widest = cfg->d_model > cfg->d_ff ? cfg->d_model : cfg->d_ff;
-    if (widest * cfg->n_experts >= (int64_t)1 << 31 || widest > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+    if (widest * cfg->n_experts >= (int64_t)1 << 31 || widest > (1 << 23)) return MOE_ERR_UNSUPPORTED;
+    // pipeline stages are counted in 32 bits: at most five row chunks per expert and 64 x 256 weights
+    // a stage (no device holds that many weights)
+    if ((int64_t)cfg->d_model * cfg->d_ff >= ((int64_t)1 << 44) / (5 * (int64_t)cfg->n_experts)) return MOE_ERR_UNSUPPORTED;
     if (!req(w.q1) || !req(w.s1) || !req(w.q2) || !req(w.s2) || !opt(w.b1) || !opt(w.b3) || !opt(w.b2))
         return MOE_ERR_INVALID_ARG;
     if (cfg->act == MOE_SWIGLU ? (!req(w.q3) || !req(w.s3)) : (!opt(w.q3) || !opt(w.s3))) return MOE_ERR_INVALID_ARG;

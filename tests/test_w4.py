@@ -81,6 +81,9 @@ def test_bad_expert_calls_are_refused():
     assert _ffn(cfg, group=48) == nat.MOE_ERR_UNSUPPORTED
     assert _ffn(nat.config(4, 128, 256, 8, 2, 4, "f32", "swiglu"), nbytes=1 << 40) == nat.MOE_ERR_UNSUPPORTED
     assert _ffn(nat.config(4, 120, 256, 8, 2, 4)) == nat.MOE_ERR_UNSUPPORTED
+    # too many weights for 32-bit counts of pipeline stages; rows longer than a launch covers
+    assert _ffn(nat.config(4, 1 << 21, 1 << 18, 8, 1, 4), nbytes=1 << 60) == nat.MOE_ERR_UNSUPPORTED
+    assert _ffn(nat.config(4, (1 << 23) + 16, 256, 8, 1, 4), nbytes=1 << 60) == nat.MOE_ERR_UNSUPPORTED
     assert _ffn(nat.config(-4, 128, 256, 8, 2, 4)) == nat.MOE_ERR_INVALID_ARG
     need = nat.moe_w4_workspace_bytes(cfg)
     assert need > nat.moe_workspace_bytes(cfg) and nat.moe_w4_workspace_bytes(nat.config(4, 128, 256, 8, 2, 4, "f32")) == 0
