@@ -18,10 +18,10 @@
 //     scales down to 2^-28 of it;
 //   x: per token, so that its largest value lies in [2^14, 2^15) -- exact for values
 //     down to 2^-29 of it (bf16 has eight bits);
-//   H: per token, from |u| <= sum |x w| <= K max|x| 8 max|s| and the biases, which no
-//     value passes.  The bound is about 2^10 (SwiGLU: 2^20) above typical values, whose
-//     fp16 form still has all its bits 2^8 below them, and 2^-12 is a sixteenth of the
-//     rounding to bf16 that the layer on bf16 weights applies here.
+//   H: per token, from |u| <= (sum |x|) 8 max|s| and the biases, which no value
+//     passes.  The bound is about 2^8 (SwiGLU: 2^16) above typical values, whose fp16
+//     form has all its bits down to 2^-14 / 2^15 = 2^-29 of it; those give 2^-12, a
+//     sixteenth of the rounding to bf16 that the layer on bf16 weights applies here.
 // The epilogues undo the powers in fp32.
 //
 // Single-lane branches around TMA, MMA and commit use elect.sync in a warp-uniform
@@ -56,6 +56,9 @@ constexpr int kXBytes = 2 * kXSub;
 constexpr int kSBytes = 2048;                     // scales of a stage: 2 boxes x 256 / G groups x 64 rows
 constexpr int kSmemTc = kWStages * (kWBytes + kSBytes) + kXStages * kXBytes + 1024;
 constexpr uint32_t kColD = 0, kColA = 2 * kTileN; // TMEM columns
+// Sums (up to 2^27 K) meet the row's power of two first: 2^-24 of it waits for the token's, so
+// that neither product leaves fp32's range for scales of 2^-91 .. 2^88 (K = 2^14) and x below 2^117.
+constexpr int kBalance = 24;
 constexpr int kNanExp = 0x7FFF;                   // exponent of a row that holds a NaN or infinity
 
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
@@ -66,6 +69,7 @@ struct TcParams {
     const __nv_bfloat16* bias_a; const __nv_bfloat16* bias_b;
     const int8_t* ea; const int8_t* eb;   // [N, m_dim] row exponents: scales were taken times 2^-e
     const int16_t* ex;                    // [R] exponents of the tokens' rows: x times 2^-ex
+    const int16_t* lx;                    // stage 1: [R] sum |x| < 2^lx
     const int32_t* top;                   // stage 1: [4][N] largest scale and bias of W1, W3 (as float bits)
     int16_t* eh;                          // stage 1: [R] exponents of H
     void* out;                            // stage 1: H [R, m_dim] fp16, stage 2: y [R, m_dim] bf16
@@ -119,13 +123,12 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e
 // exponent of a finite positive float's leading bit (0 and subnormals: -127)
 __device__ __forceinline__ int exp_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
 
-// 2^ex times this brings x to fp16 range; the exponent of the bound on |H| of a token
+// The exponent that brings a token's H to fp16 range: its bound's, less 15.
 template <int EPI>
-__device__ __forceinline__ int h_exponent(const int32_t* top, int N, int e, int ex, int k_dim) {
-    // |u| < 2^(ex + 15) k_dim 8 2^(exp(max scale) + 1), plus the bias
-    const int kbits = 32 - __clz(k_dim - 1);
+__device__ __forceinline__ int h_exponent(const int32_t* top, int N, int e, int lx) {
+    // |u| < 2^lx 8 2^(exp(max scale) + 1), plus the bias
     auto side = [&](int m) {
-        const int u = ex + 15 + kbits + 3 + exp_of(top[2 * m * N + e]) + 1, b = exp_of(top[(2 * m + 1) * N + e]) + 1;
+        const int u = lx + 3 + exp_of(top[2 * m * N + e]) + 1, b = exp_of(top[(2 * m + 1) * N + e]) + 1;
         return max(u, b) + 1;
     };
     return min(max(side(0) + (EPI == W4_SWIGLU ? side(1) : 0) - 15, -126), 126);
@@ -455,16 +458,16 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const bool in = feat < p.m_dim;
             const int n = t.n - c0;   // this group's tokens (may be none)
             const int64_t at = (int64_t)t.e * p.m_dim + feat;
-            const float up = pow2i(in ? exps[at] : 0);
+            const float up = pow2i((in ? exps[at] : 0) - kBalance);
             const float b = in && bias ? __bfloat162float(bias[at]) : 0.f;
             // the powers of two of these tokens: x's, and H's
             float* s_x = sh.scale[warp - 12][0];
             float* s_h = sh.scale[warp - 12][1];
             for (int c = lane; c < n && c < kPartN; c += 32) {
                 const int ex = p.ex[t.row0 + c0 + c];
-                s_x[c] = ex == kNanExp ? __int_as_float(0x7FC00000) : pow2i(ex);
+                s_x[c] = ex == kNanExp ? __int_as_float(0x7FC00000) : pow2i(ex + kBalance);
                 if (EPI != W4_OUT) {
-                    const int eh = h_exponent<EPI>(p.top, p.N, t.e, ex, p.k_dim);
+                    const int eh = h_exponent<EPI>(p.top, p.N, t.e, p.lx[t.row0 + c0 + c]);
                     s_h[c] = pow2i(-eh);
                     if (t.m0 == 0 && quad == 0) p.eh[t.row0 + c0 + c] = (int16_t)(ex == kNanExp ? kNanExp : eh);
                 }
@@ -523,7 +526,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 // x as fp16 rows, each times a power of two (one warp per row); clears `top`.
 __global__ void __launch_bounds__(256)
 w4_half_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ offsets, int N, int64_t R_cap,
-                    int k_dim, __half* __restrict__ out, int16_t* __restrict__ ex, int32_t* __restrict__ top) {
+                    int k_dim, __half* __restrict__ out, int16_t* __restrict__ ex, int16_t* __restrict__ lx,
+                    int32_t* __restrict__ top) {
     pdl_wait();
     pdl_launch();
     if (blockIdx.x == 0)
@@ -543,17 +547,23 @@ w4_half_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
         const float down = finite ? pow2i(-e) : 0.f;
         if (lane == 0) ex[r] = (int16_t)(finite ? e : kNanExp);
         uint4* dst = reinterpret_cast<uint4*>(out + r * k_dim);
+        float sum = 0.f;
         for (int i = lane; i < k_dim / 8; i += 32) {
             const uint4 q = finite ? src[i] : make_uint4(0, 0, 0, 0);
             const uint32_t in[4] = {q.x, q.y, q.z, q.w};
             uint32_t o[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const __half2 hh = __floats2half2_rn(bf16lo(in[k]) * down, bf16hi(in[k]) * down);
+                const float a = bf16lo(in[k]) * down, b = bf16hi(in[k]) * down;
+                sum += fabsf(a) + fabsf(b);
+                const __half2 hh = __floats2half2_rn(a, b);
                 o[k] = *reinterpret_cast<const uint32_t*>(&hh);
             }
             dst[i] = make_uint4(o[0], o[1], o[2], o[3]);
         }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) lx[r] = (int16_t)(e + exp_of(__float_as_uint(sum * 1.0625f)) + 1);   // its fp32 sum's error and more
     }
 }
 
@@ -639,13 +649,14 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     if (swiglu && !m3.make(a.w3, a.N, a.d_ff, a.d, a.group)) return cudaErrorInvalidValue;
     // exponents: x's and H's in the place of the few-row kernels' units, the weights' in their own
     int16_t* ex = reinterpret_cast<int16_t*>(a.xu);
+    int16_t* lx = ex + a.R_cap;
     int16_t* eh = reinterpret_cast<int16_t*>(a.hu);
     int8_t* e1 = a.wexp;
     int8_t* e3 = e1 + (int64_t)a.N * a.d_ff;
     int8_t* e2 = e3 + (int64_t)a.N * a.d_ff;
     const int64_t rb = (a.R_cap + 7) / 8;
     err = launch_k(w4_half_rows_kernel, dim3((unsigned)(rb < 8 * sms ? rb : 8 * sms)), dim3(256), 0, s, 1, a.xe, a.offsets,
-                   a.N, a.R_cap, a.d, reinterpret_cast<__half*>(a.xq), ex, a.top);
+                   a.N, a.R_cap, a.d, reinterpret_cast<__half*>(a.xq), ex, lx, a.top);
     if (err != cudaSuccess) return err;
     ExpArgs ea{};
     const int ng1 = (a.d + a.group - 1) / a.group, ng2 = (a.d_ff + a.group - 1) / a.group;
@@ -676,6 +687,7 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     p.ea = e1;
     p.eb = e3;
     p.ex = ex;
+    p.lx = lx;
     p.eh = eh;
     p.top = a.top;
     p.m_dim = a.d_ff;

@@ -112,6 +112,17 @@ def test_matches_definition(T, N, k, S, dtype, mask, tail):
         assert torch.equal(o[q], again[q]), f"{q} differs between two runs"
 
 
+@pytest.mark.parametrize("T,N,k,S,mask", [
+    (1, 512, 16, 1, False), (3000, 8, 8, 3, True), (4096, 32, 16, 4, True), (5000, 4, 4, 2, False), (20000, 128, 3, 1, True),
+    (9000, 16, 16, 2, True), (3000, 16, 2, 3000, False), (260, 200, 5, 260, True), (100000, 256, 8, 1, True)])
+def test_tiles_batches_and_units(T, N, k, S, mask):
+    # several tiles summed by the last of them, more choices than are loaded ahead, sequences of a row
+    # or none that cut every batch, one sequence over all tiles
+    h, idx, seqs, m = make(T, N, k, S, "f32", seed=T, mask=mask)
+    for _ in range(2):
+        check(h, idx, seqs, m, "f32", run(h, idx, seqs, m, "f32"))
+
+
 def test_one_group_without_offsets():
     h, idx, _, _ = make(999, 24, 3, 1, "f32", mask=False)
     o = run(h, idx, None, None, "f32")

@@ -202,6 +202,71 @@ def test_expert_ffn_many_rows(act, group, d, dff, rows):
     assert torch.equal(y, run_ffn(dev, x, off, N, d, dff, group, act, off[-1] + 40)), "two runs differ"
 
 
+@pytest.mark.parametrize("act,group", [("relu", 128), ("swiglu", 32)])
+@pytest.mark.parametrize("N,d,dff,most", [
+    (1, 128, 128, 16), (1, 128, 128, 17), (1, 16, 16, 40), (1, 48, 272, 193), (2, 272, 16, 33), (128, 64, 48, 5), (128, 16, 144, 40)])
+def test_expert_ffn_at_the_edges(N, d, dff, most, act, group):
+    # one expert and 128, both sides of the rows that decide between the kernels, K of a single block
+    rng = np.random.default_rng(d + most)
+    rows = rng.integers(0, most + 1, N)
+    rows[-1] = most
+    off = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    W, dev = make_experts(N, d, dff, group, act, True, seed=d)
+    x = make_rows(off[-1], d)
+    y = run_ffn(dev, x, off, N, d, dff, group, act, off[-1])
+    check_ffn(W, x, y, off, group, act)
+
+
+@pytest.mark.parametrize("rows", [[3, 2], [70, 200]])
+@pytest.mark.parametrize("act", ["relu", "swiglu"])
+def test_magnitudes_far_from_one(act, rows):
+    # rows of x and of the weights at very different powers of two (H and y stay within 2^+-100);
+    # with SwiGLU a channel of x and two weight rows far above the others
+    N, d, dff, group = 2, 256, 320, 64
+    W, dev = make_experts(N, d, dff, group, act, False, seed=3)
+    rng = np.random.default_rng(4)
+    off = np.concatenate([[0], np.cumsum(rows)]).tolist()
+    x = make_rows(off[-1], d).double()
+    if act == "relu":
+        x *= torch.from_numpy(2.0 ** rng.integers(-40, 41, (off[-1], 1)))
+        for n in ("w1", "w2"):
+            W[n] = (W[n][0], W[n][1] * 2.0 ** rng.integers(-25, 26, (N, 1, W[n][1].shape[2])))
+    else:
+        x[:, 7] *= 1000
+        W["w1"][1][:, :, 3] *= 64
+        W["w3"][1][:, :, 5] *= 64
+    for n in ("w1", "w3", "w2"):
+        if W[n] is not None:
+            dev[n] = (dev[n][0], torch.from_numpy(W[n][1]).to(torch.bfloat16).cuda())
+    x = x.to(torch.bfloat16)
+    y = run_ffn(dev, x, off, N, d, dff, group, act, off[-1])
+    check_ffn(W, x, y, off, group, act)
+
+
+def test_one_workspace_for_both_kinds_of_experts():
+    # the layer on bf16 and on 4-bit experts in turn, few and many rows: each gives what it gives alone
+    N, d, dff, group = 4, 128, 272, 32
+    W, dev = make_experts(N, d, dff, group, "swiglu", False, seed=5)
+    wb = [torch.randn(N, *W[n][0].shape[1:], device="cuda").bfloat16() * 0.05 for n in ("w1", "w3", "w2")]
+    for T in (5, 400):
+        L = inputs.make_layer(T=T, d_model=d, d_ff=16, n_experts=N, top_k=2, dtype="bf16", seed=T)
+        cfg = nat.config(T, d, dff, N, 2, T, "bf16", "swiglu")
+        x, w_r, b_r = layer_args(L)
+
+        def both(ws_a, ws_b):
+            outs = [torch.empty(T, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+            nat.check(nat.moe_forward(cfg, x, w_r, b_r, wb[0], None, wb[1], None, wb[2], None, outs[0], ws=ws_a))
+            nat.check(nat.moe_forward_w4(cfg, group, x, w_r, b_r, *weight_args(dev), outs[1], ws=ws_b))
+            return outs
+
+        want = both(nat.new_workspace(cfg), nat.new_w4_workspace(cfg))
+        ws = nat.new_w4_workspace(cfg)
+        for _ in range(3):
+            for got, ref in zip(both(ws, ws), want):
+                assert torch.equal(got, ref)
+        nat.check(nat.moe_read_device_status(ws))
+
+
 def test_a_rows_result_does_not_depend_on_other_experts_rows():
     N, d, dff, group = 3, 256, 320, 64
     W, dev = make_experts(N, d, dff, group, "swiglu", True)
