@@ -45,17 +45,25 @@ using namespace tc;
 namespace {
 
 constexpr int kThreadsTc = 640;
-constexpr int kTileN = 192;                       // tokens of a tile
-constexpr int kPartN = kTileN / 2;                // ... of a group of writing warps
 constexpr int kBoxN = 64;                         // tokens per TMA box
+constexpr int kBoxBytes = kBoxN * 128;            // ... by 64 of K
 constexpr int kWStages = 4;                       // packed rows and scales: 256 of K each
-constexpr int kXStages = 3;                       // tokens: 128 of K each
 constexpr int kWBytes = 128 * 128;
-constexpr int kXSub = kTileN * 128;               // 64 of K
-constexpr int kXBytes = 2 * kXSub;
 constexpr int kSBytes = 2048;                     // scales of a stage: 2 boxes x 256 / G groups x 64 rows
-constexpr int kSmemTc = kWStages * (kWBytes + kSBytes) + kXStages * kXBytes + 1024;
-constexpr uint32_t kColD = 0, kColA = 2 * kTileN; // TMEM columns
+
+// Tiles of up to 192 tokens, whose accumulator has a second one beside it in TMEM; or (WIDE) of up to
+// 256, one accumulator, so that nothing accumulates while a tile is written out.
+template <bool WIDE>
+struct Shape {
+    static constexpr int N = WIDE ? 256 : 192;            // tokens of a tile
+    static constexpr int PART = N / 2;                    // ... of a group of writing warps
+    static constexpr int D = WIDE ? 1 : 2;                // accumulators
+    static constexpr uint32_t COL_D = 0, COL_A = D * N;   // TMEM columns
+    static constexpr int XSTAGES = WIDE ? 2 : 3;          // tokens: 128 of K each
+    static constexpr int XSUB = N / kBoxN * kBoxBytes;    // 64 of K
+    static constexpr int XBYTES = 2 * XSUB;
+    static constexpr int SMEM = kWStages * (kWBytes + kSBytes) + XSTAGES * XBYTES + 1024;
+};
 // Sums (up to 2^27 K) meet the row's power of two first: 2^-24 of it waits for the token's, so
 // that neither product leaves fp32's range for scales of 2^-91 .. 2^88 (K = 2^14) and x below 2^117.
 constexpr int kBalance = 24;
@@ -134,29 +142,31 @@ __device__ __forceinline__ int h_exponent(const int32_t* top, int N, int e, int 
     return min(max(side(0) + (EPI == W4_SWIGLU ? side(1) : 0) - 15, -126), 126);
 }
 
+template <bool WIDE>
 struct SharedTc {
     uint64_t wfull[kWStages], wempty[kWStages];
-    uint64_t xfull[kXStages], xempty[kXStages];
+    uint64_t xfull[Shape<WIDE>::XSTAGES], xempty[Shape<WIDE>::XSTAGES];
     uint64_t afull[2], mdone[2];    // a block's weights are in TMEM; its MMAs are done
     uint64_t dfull[2], dempty[2];   // accumulators of a tile
     uint64_t done;
     uint32_t tmem;
     int abort, live;
     int row[129], exp[128], first[129];
-    float scale[8][2][kPartN];      // per writing warp: the tokens' powers of two
+    float scale[8][2][Shape<WIDE>::PART];      // per writing warp: the tokens' powers of two
 };
 
 struct Tile {
     int e, m0, row0, n;
 };
 
-// rows of an expert in equal chunks of at most 192, a multiple of 16
-__device__ __forceinline__ int chunk_rows(int n) {
-    const int chunks = (n + kTileN - 1) / kTileN;
+// rows of an expert in equal chunks of at most `most`, a multiple of 16
+__device__ __forceinline__ int chunk_rows(int n, int most) {
+    const int chunks = (n + most - 1) / most;
     return ((n + chunks - 1) / chunks + 15) / 16 * 16;
 }
 
-__device__ __forceinline__ Tile tile_of(const SharedTc& sh, int u, int feats) {
+template <bool WIDE>
+__device__ __forceinline__ Tile tile_of(const SharedTc<WIDE>& sh, int u, int feats) {
     int lo = 0, hi = sh.live;   // first[lo] <= u < first[hi]
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -164,7 +174,7 @@ __device__ __forceinline__ Tile tile_of(const SharedTc& sh, int u, int feats) {
         else hi = mid;
     }
     const int e = sh.exp[lo], rows = sh.row[e + 1] - sh.row[e], local = u - sh.first[lo];
-    const int per = chunk_rows(rows), chunks = (rows + per - 1) / per;
+    const int per = chunk_rows(rows, Shape<WIDE>::N), chunks = (rows + per - 1) / per;
     Tile t;   // the chunks of a feature tile follow one another: its weights are in L2
     t.e = e;
     t.m0 = local / chunks * feats;
@@ -173,7 +183,7 @@ __device__ __forceinline__ Tile tile_of(const SharedTc& sh, int u, int feats) {
     return t;
 }
 
-template <int EPI, int G>
+template <int EPI, int G, bool WIDE>
 __global__ void __launch_bounds__(kThreadsTc, 1)
 w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
              const __grid_constant__ CUtensorMap map_sa, const __grid_constant__ CUtensorMap map_sb,
@@ -181,18 +191,19 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     constexpr int MATS = EPI == W4_SWIGLU ? 2 : 1;
     constexpr int FEATS = 128 / MATS;
     constexpr int PER = kW4Block / G;   // groups per 128 of K
+    using S = Shape<WIDE>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     uint8_t* smem_x = smem + kWStages * kWBytes;
-    uint8_t* smem_s = smem_x + kXStages * kXBytes;
-    __shared__ __align__(8) SharedTc sh;
+    uint8_t* smem_s = smem_x + S::XSTAGES * S::XBYTES;
+    __shared__ __align__(8) SharedTc<WIDE> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < kWStages; ++s) {
             mbar_init(smem_u32(&sh.wfull[s]), 1);
             mbar_init(smem_u32(&sh.wempty[s]), 8);
         }
-        for (int s = 0; s < kXStages; ++s) {
+        for (int s = 0; s < S::XSTAGES; ++s) {
             mbar_init(smem_u32(&sh.xfull[s]), 1);
             mbar_init(smem_u32(&sh.xempty[s]), 1);
         }
@@ -222,7 +233,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int e = 4 * lane + i, rows = e < p.N ? max(0, sh.row[e + 1] - sh.row[e]) : 0;
-            n[i] = rows == 0 ? 0 : (rows + chunk_rows(rows) - 1) / chunk_rows(rows) * tiles;
+            const int per = chunk_rows(max(rows, 1), S::N);
+            n[i] = (rows + per - 1) / per * tiles;
             live += n[i] > 0;
             units += n[i];
         }
@@ -270,26 +282,26 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     if (mine) {
                         ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.xempty[xs]), xph ^ 1u, w));
                         if (!ok) break;
-                        const uint32_t fb = smem_u32(&sh.xfull[xs]), dst = smem_u32(smem_x) + xs * kXBytes;
+                        const uint32_t fb = smem_u32(&sh.xfull[xs]), dst = smem_u32(smem_x) + xs * S::XBYTES;
                         const int halves = kb * kW4Block + 64 < p.k_dim ? 2 : 1;
                         if (elect_one()) {
-                            mbar_expect_tx(fb, halves * boxes * kBoxN * 128);
+                            mbar_expect_tx(fb, halves * boxes * kBoxBytes);
                             for (int h = 0; h < halves; ++h)
                                 for (int b = 0; b < boxes; ++b)
-                                    tma_load_2d(dst + h * kXSub + b * kBoxN * 128, &map_x, fb, kb * kW4Block + h * 64,
+                                    tma_load_2d(dst + h * S::XSUB + b * kBoxBytes, &map_x, fb, kb * kW4Block + h * 64,
                                                 t.row0 + b * kBoxN);
                         }
                         __syncwarp();
                     }
                     xused |= 1u << xs;
-                    if (++xs == kXStages) {
+                    if (++xs == S::XSTAGES) {
                         xs = 0;
                         xph ^= 1u;
                     }
                 }
             }
             // every load has landed before the CTA retires (each warp looks at all stages)
-            for (int s = 0; s < kXStages; ++s)
+            for (int s = 0; s < S::XSTAGES; ++s)
                 if (xused >> s & 1u) drain_bar(smem_u32(&sh.xfull[s]), s < xs ? xph : xph ^ 1u, p.limit_ns, p.status);
         } else if (warp == 2) {
             // ---------------- TMA: packed rows and scales ----------------
@@ -338,21 +350,21 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 const Tile t = tile_of(sh, u, FEATS);
                 const uint32_t idesc = idesc_f16_f32(128, (t.n + 15) / 16 * 16);
                 if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.dempty[d]), dph ^ 1u, w)))) break;
-                const uint32_t dd = tmem + kColD + d * kTileN;
+                const uint32_t dd = tmem + S::COL_D + d * S::N;
                 for (int kb = 0; kb < nb; ++kb) {
                     ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.afull[a]), aph, w) &&
                                                      wait_bar_soon(smem_u32(&sh.xfull[xs]), xph, w));
                     if (!ok) break;
                     tc_fence_after();
                     issued = true;
-                    const uint64_t bd = bd0 + (uint64_t)(xs * (kXBytes >> 4));
-                    const uint32_t ad = tmem + kColA + a * 64;
+                    const uint64_t bd = bd0 + (uint64_t)(xs * (S::XBYTES >> 4));
+                    const uint32_t ad = tmem + S::COL_A + a * 64;
                     const int nk = min(8, (p.k_dim - kb * kW4Block) / 16);   // K is a multiple of 16
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             if (kk < nk)
-                                umma_ts(dd, ad + 8 * kk, bd + (uint64_t)((kk / 4 * kXSub) >> 4) + 2 * (kk % 4), idesc, kb | kk);
+                                umma_ts(dd, ad + 8 * kk, bd + (uint64_t)((kk / 4 * S::XSUB) >> 4) + 2 * (kk % 4), idesc, kb | kk);
                         umma_commit(smem_u32(&sh.mdone[a]));
                         umma_commit(smem_u32(&sh.xempty[xs]));
                         if (kb + 1 == nb) umma_commit(smem_u32(&sh.dfull[d]));
@@ -360,13 +372,15 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     __syncwarp();
                     a ^= 1;
                     if (a == 0) aph ^= 1u;
-                    if (++xs == kXStages) {
+                    if (++xs == S::XSTAGES) {
                         xs = 0;
                         xph ^= 1u;
                     }
                 }
-                d ^= 1;
-                if (d == 0) dph ^= 1u;
+                if (++d == S::D) {
+                    d = 0;
+                    dph ^= 1u;
+                }
             }
             if (issued) {   // every MMA has completed before TMEM is freed
                 if (elect_one()) umma_commit(smem_u32(&sh.done));
@@ -388,7 +402,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         // its scales in a stage: box, then 64 features a group
         const int soff = ((r >> 6) * (2 * PER * 64) + (r & 63)) * 2;
         const int8_t* exps = MATS == 2 && lane >= 16 ? p.eb : p.ea;
-        const uint32_t dst = tmem + kColA + a * 64 + ((uint32_t)(quad * 32) << 16);
+        const uint32_t dst = tmem + S::COL_A + a * 64 + ((uint32_t)(quad * 32) << 16);
         int ws = 0, turn = 0;
         uint32_t wph = 0, aph = 0;
         bool ok = true;
@@ -444,7 +458,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
     } else {
         // ---------------- write out: lane = weight row ----------------
         // two groups of four warps, 96 of the tile's tokens each
-        const int quad = warp & 3, c0 = (warp - 12) / 4 * kPartN;
+        const int quad = warp & 3, c0 = (warp - 12) / 4 * S::PART;
         const int f = MATS == 2 ? quad * 16 + (lane & 15) : quad * 32 + lane;   // feature of the tile
         const bool low = lane < 16;
         const __nv_bfloat16* bias = MATS == 2 && !low ? p.bias_b : p.bias_a;
@@ -463,7 +477,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             // the powers of two of these tokens: x's, and H's
             float* s_x = sh.scale[warp - 12][0];
             float* s_h = sh.scale[warp - 12][1];
-            for (int c = lane; c < n && c < kPartN; c += 32) {
+            for (int c = lane; c < n && c < S::PART; c += 32) {
                 const int ex = p.ex[t.row0 + c0 + c];
                 s_x[c] = ex == kNanExp ? __int_as_float(0x7FC00000) : pow2i(ex + kBalance);
                 if (EPI != W4_OUT) {
@@ -475,9 +489,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             __syncwarp();
             if (!(ok = __all_sync(0xffffffffu, wait_bar_soon(smem_u32(&sh.dfull[d]), dph, w)))) break;
             tc_fence_after();
-            const uint32_t src = tmem + kColD + d * kTileN + c0 + ((uint32_t)(quad * 32) << 16);
+            const uint32_t src = tmem + S::COL_D + d * S::N + c0 + ((uint32_t)(quad * 32) << 16);
 #pragma unroll 1
-            for (int cb = 0; cb < kPartN && cb < n; cb += 32) {
+            for (int cb = 0; cb < S::PART && cb < n; cb += 32) {
                 uint32_t v[32];
                 tmem_ld32(src + cb, v);
                 tmem_wait_ld();
@@ -513,8 +527,10 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_relaxed(smem_u32(&sh.dempty[d]));
-            d ^= 1;
-            if (d == 0) dph ^= 1u;
+            if (++d == S::D) {
+                d = 0;
+                dph ^= 1u;
+            }
         }
     }
     tc_fence_before();
@@ -605,15 +621,15 @@ w4_exponent_kernel(const ExpArgs a) {
     }
 }
 
-template <int EPI, int G>
+template <int EPI, int G, bool WIDE>
 cudaError_t run_tc_g(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& sa, const CUtensorMap& sb,
                      const CUtensorMap& x, const TcParams& p, int sms, cudaStream_t s) {
-    auto kern = w4_tc_kernel<EPI, G>;
+    auto kern = w4_tc_kernel<EPI, G, WIDE>;
     cudaError_t err = once_per_device(reinterpret_cast<const void*>(kern), [](const void* k) {
-        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemTc);
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<WIDE>::SMEM);
     });
     if (err != cudaSuccess) return err;
-    return launch_k(kern, dim3((unsigned)sms), dim3(kThreadsTc), kSmemTc, s, 1, a, b, sa, sb, x, p);
+    return launch_k(kern, dim3((unsigned)sms), dim3(kThreadsTc), Shape<WIDE>::SMEM, s, 1, a, b, sa, sb, x, p);
 }
 
 // one matrix of a stage: its packed rows and its scales
@@ -625,12 +641,20 @@ struct Maps {
     }
 };
 
+template <int EPI, bool WIDE>
+cudaError_t run_tc_w(const Maps& a, const Maps& b, const CUtensorMap& x, const TcParams& p, int group, int sms,
+                     cudaStream_t s) {
+    if (group == 32) return run_tc_g<EPI, 32, WIDE>(a.q, b.q, a.s, b.s, x, p, sms, s);
+    if (group == 64) return run_tc_g<EPI, 64, WIDE>(a.q, b.q, a.s, b.s, x, p, sms, s);
+    return run_tc_g<EPI, 128, WIDE>(a.q, b.q, a.s, b.s, x, p, sms, s);
+}
+
 template <int EPI>
 cudaError_t run_tc(const Maps& a, const Maps& b, const CUtensorMap& x, const TcParams& p, int group, int sms,
                    cudaStream_t s) {
-    if (group == 32) return run_tc_g<EPI, 32>(a.q, b.q, a.s, b.s, x, p, sms, s);
-    if (group == 64) return run_tc_g<EPI, 64>(a.q, b.q, a.s, b.s, x, p, sms, s);
-    return run_tc_g<EPI, 128>(a.q, b.q, a.s, b.s, x, p, sms, s);
+    const int64_t rows = (p.R_cap + p.N - 1) / p.N;   // of an expert, on average
+    const bool wide = (rows + Shape<true>::N - 1) / Shape<true>::N < (rows + Shape<false>::N - 1) / Shape<false>::N;
+    return wide ? run_tc_w<EPI, true>(a, b, x, p, group, sms, s) : run_tc_w<EPI, false>(a, b, x, p, group, sms, s);
 }
 
 }  // namespace

@@ -192,7 +192,8 @@ def test_expert_ffn(d, dff, rows, bias, group, act):
 
 @pytest.mark.parametrize("act,group,d,dff,rows", [
     ("swiglu", 128, 512, 896, [200, 0, 64, 129, 1, 256]), ("relu", 32, 384, 640, [300, 65, 130]),
-    ("swiglu", 64, 272, 528, [128, 127, 66]), ("relu", 128, 1024, 272, [513, 2]), ("swiglu", 32, 160, 144, [257, 70])])
+    ("swiglu", 64, 272, 528, [128, 127, 66]), ("swiglu", 128, 208, 144, [192, 193, 208, 0, 384, 385, 321]),
+    ("relu", 64, 64, 272, [383, 96, 97, 224, 16]), ("relu", 32, 144, 2064, [260, 800]), ("relu", 128, 1024, 272, [513, 2]), ("swiglu", 32, 160, 144, [257, 70])])
 def test_expert_ffn_many_rows(act, group, d, dff, rows):
     N, off = len(rows), np.concatenate([[0], np.cumsum(rows)]).tolist()
     W, dev = make_experts(N, d, dff, group, act, True, seed=d)
