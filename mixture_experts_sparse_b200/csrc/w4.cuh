@@ -7,7 +7,7 @@
 // by word, the A fragments of m16n8k32 for 32 consecutive k, and a group scale
 // never cuts a fragment; (b) the even and the odd nibbles of a word, as the upper
 // halves of four bytes each, are 16 q in two's complement after one exclusive or;
-// (c) one shift and one logic operation give an adjacent pair as bf16.
+// (c) one logic operation on the word, or on it shifted by 8, gives an adjacent pair as fp16.
 // Scales are bf16, [matrix][group][row]: the scales of a tile's rows are adjacent.
 #pragma once
 
@@ -46,7 +46,7 @@ struct W4FfnArgs {
     float* xu;             // [R_cap][w4_padded(d) / 64]: their units
     uint8_t* hq;           // [R_cap][w4_padded(d_ff)] x 2 bytes: H
     float* hu;
-    void* h;               // [R_cap, d_ff] fp16: H, many rows (whose x is in xq, exponents in xu, hu)
+    void* h;               // many rows: H as fp16 [R_cap, d_ff]; x as fp16 is in xq, exponents in xu and hu
     int8_t* wexp;          // [N, d_ff] twice and [N, d]: the weight rows' exponents
     int32_t* top;          // [4][N]
     __nv_bfloat16* ye;     // [R_cap, d]
