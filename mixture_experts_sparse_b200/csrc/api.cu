@@ -57,7 +57,7 @@ namespace {
 size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 struct Layout {
-    size_t hdr, w4_count, part_cnt, part_psum, part_z, w_split, scan_state;
+    size_t hdr, part_cnt, part_psum, part_z, w_split, scan_state;
     size_t idx, gate, pos, drop, counts, kept, offsets, f, P, aux;
     size_t row_token, row_gate, xe, h, ye;
     size_t prio_hist, prio_cursor, prio_list, prio_perm, prio_idx, prio_pos, prio_range;   // batch priority only
@@ -88,7 +88,6 @@ Layout layout_of(const moe_config& c) {
     L.rows = compact_rows(c);
     const size_t R = (size_t)(L.rows > 0 ? L.rows : 1);
     L.hdr = take(sizeof(WsHeader));
-    L.w4_count = take(4 * 2 * kW4Counters);
     const size_t nbr = (size_t)router_partial_rows(c.T, c.n_experts);
     L.part_cnt = take(4 * nbr * N);
     L.part_psum = take(4 * nbr * N);
@@ -228,9 +227,7 @@ size_t moe_workspace_bytes(const moe_config* cfg) {
 
 int32_t moe_workspace_init(void* ws, size_t ws_bytes, void* stream) {
     if (!ws || !aligned(ws) || ws_bytes < sizeof(WsHeader)) return MOE_ERR_WORKSPACE;
-    // the header and, in a layer workspace, the arrival counters behind it
-    const size_t clear = sizeof(WsHeader) + 4 * 2 * kW4Counters;
-    return cuda_status(cudaMemsetAsync(ws, 0, ws_bytes < clear ? ws_bytes : clear, (cudaStream_t)stream));
+    return cuda_status(cudaMemsetAsync(ws, 0, sizeof(WsHeader), (cudaStream_t)stream));
 }
 
 const char* moe_status_string(int32_t status) {
@@ -714,7 +711,7 @@ static bool w4_group_ok(int32_t g) { return g == 32 || g == 64 || g == 128; }
 // the layer workspace, then the rows of x and H as integers with their units, then
 // the sums of tiles that CTAs share
 struct W4Layout {
-    size_t xq, xu, hq, hu, part, wexp, top, total;
+    size_t xq, xu, hq, hu, part, count, wexp, top, total;
 };
 static W4Layout w4_layout(const moe_config& c, const Layout& L) {
     W4Layout w{};
@@ -731,6 +728,7 @@ static W4Layout w4_layout(const moe_config& c, const Layout& L) {
     w.hq = take(2 * R * f);
     w.hu = take(4 * R * (f / kW4ActBlock));
     w.part = take((size_t)w4_part_bytes());
+    w.count = take(4 * 2 * kW4Counters);
     w.wexp = take((size_t)c.n_experts * (2 * (size_t)c.d_ff + (size_t)c.d_model));
     w.top = take(4 * 4 * (size_t)c.n_experts);
     w.total = off;
@@ -820,7 +818,7 @@ static int32_t w4_ffn_impl(const moe_config* cfg, const W4Weights& w, const void
     a.top = at<int32_t>(ws, W.top);
     a.ye = static_cast<__nv_bfloat16*>(ye);
     a.part = at<float>(ws, W.part);
-    a.count = at<int32_t>(ws, L.w4_count);
+    a.count = at<int32_t>(ws, W.count);
     a.hdr = at<WsHeader>(ws, L.hdr);
     return cuda_status(launch_w4_ffn(a, s));
 }

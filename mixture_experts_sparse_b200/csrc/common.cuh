@@ -27,10 +27,6 @@ struct WsHeader {
     int32_t pad[59];
 };
 static_assert(sizeof(WsHeader) == 256, "header size");
-// Behind the header of a layer workspace: arrival counters of the 4-bit expert
-// kernels, one per CTA for each of their two launches.  moe_workspace_init
-// clears them; the kernels leave them at zero.
-constexpr int kW4Counters = 512;
 
 // Default limit of every device-side bounded wait: far above any legitimate
 // wait (microseconds), low enough that a wedged wait returns promptly.

@@ -17,6 +17,7 @@ namespace moe {
 
 constexpr int kW4Block = 128;        // weights per block
 constexpr int kW4BlockBytes = 64;
+constexpr int kW4Counters = 512;     // arrival counters of a few-row launch, one per CTA
 
 inline int64_t w4_blocks(int64_t k) { return (k + kW4Block - 1) / kW4Block; }
 inline int64_t w4_row_bytes(int64_t k) { return w4_blocks(k) * kW4BlockBytes; }
@@ -51,7 +52,7 @@ struct W4FfnArgs {
     int32_t* top;          // [4][N]
     __nv_bfloat16* ye;     // [R_cap, d]
     float* part;           // w4_part_bytes(): sums of tiles that CTAs share
-    int32_t* count;        // [2][kW4Counters], zero between calls
+    int32_t* count;        // [2][kW4Counters], cleared by every call
     WsHeader* hdr;
 };
 int w4_gemv_ctas(int sms);

@@ -69,9 +69,7 @@ struct GemvParams {
     __nv_bfloat16* out;                                  // stage 2: [R, m_dim]
     uint8_t* hq; float* hu;                              // stage 1: H as integers
     float* part;                  // [CTAs][2][kPartFloats]
-    int32_t* count;               // [CTAs] arrivals per shared tile, zero between calls
-    int32_t* clear;               // [clear_n] the other stage's counters
-    int clear_n;
+    int32_t* count;               // [CTAs] arrivals per shared tile, zero at the start
     int smem_bytes;               // dynamic shared memory of a CTA
     int32_t* status;
     long long limit_ns;
@@ -433,7 +431,6 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const R
                 __threadfence();
                 const int before = atomicAdd(p.count + c0, 1);
                 sh.last = before == c1 - c0;
-                if (before == c1 - c0) p.count[c0] = 0;
                 __threadfence();
             }
             named_bar(1, kRows);
@@ -506,14 +503,16 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const R
 }
 
 // Rows of x as integers: eight lanes per 64 values, whose unit is that of their
-// block of UB (64 or 128).
+// block of UB (64 or 128).  Clears both stages' counters, whatever the workspace held.
 constexpr int kRowThreads = 256;
 template <int UB>
 __global__ void __launch_bounds__(kRowThreads)
 w4_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ offsets, int N, int64_t R_cap, int k_dim,
-               uint8_t* __restrict__ xq, float* __restrict__ xu) {
+               uint8_t* __restrict__ xq, float* __restrict__ xu, int32_t* __restrict__ count) {
     pdl_wait();
     pdl_launch();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < 2 * kW4Counters; i += kRowThreads) count[i] = 0;
     const int64_t last = offsets[N], rows = last < 0 ? 0 : (last > R_cap ? R_cap : last);
     const int64_t padded = w4_padded(k_dim);
     const int blocks = (int)(padded / kW4ActBlock), l = threadIdx.x & 7;
@@ -655,10 +654,6 @@ w4_gemv_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
     __syncthreads();
     run_tiles<EPI, G, UB>(p, &map_a, &map_b, sh, smem);
-    // The other stage's counters: stage 1 clears stage 2's, whose parts come after
-    // it, and stage 2 (past its wait) those of the next call's stage 1.
-    if (blockIdx.x == 0)
-        for (int i = tid; i < p.clear_n; i += kThreads) p.clear[i] = 0;
 }
 
 // packed rows [rows][pitch] bytes: boxes of 64 rows x 128 bytes, 128-byte swizzle
@@ -710,7 +705,6 @@ cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     p.part = a.part;
     p.status = &a.hdr->status;
     p.limit_ns = kWaitLimitNs;
-    p.clear_n = w4_gemv_ctas(sms);
     p.m_dim = a.d_ff;
     p.k_dim = a.d;
     p.sa = a.w1.s;
@@ -722,11 +716,10 @@ cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     p.hq = a.hq;
     p.hu = a.hu;
     p.count = a.count;
-    p.clear = a.count + kW4Counters;
     const int64_t row_blocks = (a.R_cap * (w4_padded(a.d) / kW4ActBlock) + kRowThreads / 8 - 1) / (kRowThreads / 8);
     err = launch_k(a.group == 128 ? w4_rows_kernel<128> : w4_rows_kernel<64>,
                    dim3((unsigned)(row_blocks < 8 * sms ? row_blocks : 8 * sms)), dim3(kRowThreads), 0, s, 1, a.xe, a.offsets,
-                   a.N, a.R_cap, a.d, a.xq, a.xu);
+                   a.N, a.R_cap, a.d, a.xq, a.xu, a.count);
     if (err != cudaSuccess) return err;
     err = a.act == MOE_SWIGLU ? run_gemv<W4_SWIGLU, 128>(m1, m3, p, a.group, sms, s)
                               : run_gemv<W4_RELU, 128>(m1, m3, p, a.group, sms, s);
@@ -740,7 +733,6 @@ cudaError_t launch_w4_ffn(const W4FfnArgs& a, cudaStream_t s) {
     p.xu = a.hu;
     p.out = a.ye;
     p.count = a.count + kW4Counters;
-    p.clear = a.count;
     return a.act == MOE_SWIGLU ? run_gemv<W4_OUT, 64>(m2, m2, p, a.group, sms, s)
                                : run_gemv<W4_OUT, 128>(m2, m2, p, a.group, sms, s);
 }

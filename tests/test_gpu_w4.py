@@ -268,6 +268,20 @@ def test_one_workspace_for_both_kinds_of_experts():
         nat.check(nat.moe_read_device_status(ws))
 
 
+@pytest.mark.parametrize("rows", [[3, 2, 4], [40, 30, 60]])
+def test_a_workspace_may_have_held_anything(rows):
+    # past its header, in either kernel
+    N, d, dff, group, R = 3, 512, 1040, 64, sum(rows)
+    W, dev = make_experts(N, d, dff, group, "swiglu", True)
+    x, offsets = make_rows(R, d), [0, rows[0], rows[0] + rows[1], R]
+    want = run_ffn(dev, x, offsets, N, d, dff, group, "swiglu", R)
+    for fill in (0xFF, 0x01):
+        ws = nat.new_w4_workspace(nat.config(R, d, dff, N, 1, R, "bf16", "swiglu"))
+        ws[256:] = fill
+        for _ in range(2):
+            assert torch.equal(run_ffn(dev, x, offsets, N, d, dff, group, "swiglu", R, ws=ws), want)
+
+
 def test_a_rows_result_does_not_depend_on_other_experts_rows():
     N, d, dff, group = 3, 256, 320, 64
     W, dev = make_experts(N, d, dff, group, "swiglu", True)
