@@ -67,6 +67,12 @@ __device__ __forceinline__ bool wait_bar_soon(uint32_t bar, uint32_t parity, con
     return wait_bar(bar, parity, w);
 }
 
+// Two of them; the tries overlap where both phases have ended.
+__device__ __forceinline__ bool wait_two(uint32_t bar0, uint32_t parity0, uint32_t bar1, uint32_t parity1, const Waiter& w) {
+    const bool a = mbar_try(bar0, parity0), b = mbar_try(bar1, parity1);
+    return (a || wait_bar_soon(bar0, parity0, w)) && (b || wait_bar_soon(bar1, parity1, w));
+}
+
 // Teardown wait: ignores the abort flag, still bounded.
 __device__ __forceinline__ bool drain_bar(uint32_t bar, uint32_t parity, long long limit, int32_t* status) {
     const long long t0 = global_ns();
