@@ -26,7 +26,7 @@
 //
 // Single-lane branches around TMA, MMA and commit use elect.sync in a warp-uniform
 // loop: with `lane == 0` each such instruction took 45 cycles to issue, not 9.
-// 1024 tokens of the d_model 4096 layer, 256 rows an expert on average: 0.72 ms, 1.0
+// 1024 tokens of the d_model 4096 layer, 256 rows an expert on average: 0.70 ms, 1.0
 // PFLOP/s; the same rows spread evenly 0.60 ms.  With few tokens a tile (32 rows an
 // expert: 0.37 ms) a block's hand-overs between the roles bound it, not its MMAs.
 //
@@ -600,7 +600,7 @@ w4_half_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
         if (lane == 0) ex[r] = (int16_t)(finite ? e : kNanExp);
         uint4* dst = reinterpret_cast<uint4*>(out + r * k_dim);
         float sum = 0.f;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = lane; i < k_dim / 8; i += 32) {
             uint4 q = __ldg(src + i);
             if (!finite) q = make_uint4(0, 0, 0, 0);
@@ -622,9 +622,11 @@ w4_half_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
 }
 
 // Every weight row's exponent: its largest finite scale times 2^-e lies in [2^11, 2^12);
-// and of W1, W3 the largest scale and bias of the expert.  A block takes 128 rows, sixteen
-// threads eight of them each, sixteen slices of the groups (a thread per row waited for one
-// load after the other: 37 us for the d_model 4096 layer's 22 MB of scales).
+// and of W1, W3 the largest scale and bias of the expert.  A thread takes eight rows and a
+// slice of the groups, eight loads in flight (a thread per row waited for one load after the
+// other: 37 us for the d_model 4096 layer's 22 MB of scales).  Four slices of groups of 128,
+// sixteen of shorter ones: 32 rows an expert of that layer, groups of 128, take 355 us with 4
+// slices and 368 with 16, its ReLU form with groups of 32 314 and 294.
 // It runs beside the conversion of x, whose launch follows the end of all earlier work: the
 // weights' arrays are read and the exponents written before the wait, `top` only behind it.
 struct ExpArgs {
@@ -634,15 +636,18 @@ struct ExpArgs {
     const int32_t* offsets; int N;
     int32_t* top;
 };
-constexpr int kExpRows = 128;
-__global__ void __launch_bounds__(256)
+constexpr int kExpThreads = 256;
+template <int SLICES> constexpr int kExpRows = kExpThreads / SLICES * 8;   // of a block
+template <int SLICES>
+__global__ void __launch_bounds__(kExpThreads)
 w4_exponent_kernel(const ExpArgs a) {
-    __shared__ uint4 sh[16][16];
-    const int m = blockIdx.z, e = blockIdx.y, l = threadIdx.x & 15, slice = threadIdx.x >> 4;
-    const int rows = a.rows[m], row = blockIdx.x * kExpRows + 8 * l;   // rows are multiples of 16
+    constexpr int LANES = kExpThreads / SLICES;
+    __shared__ uint4 sh[SLICES][LANES];
+    const int m = blockIdx.z, e = blockIdx.y, l = threadIdx.x % LANES, slice = threadIdx.x / LANES;
+    const int rows = a.rows[m], row = blockIdx.x * kExpRows<SLICES> + 8 * l;   // rows are multiples of 16
     uint32_t bias = 0;
     uint32_t big[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const bool live = a.s[m] != nullptr && a.offsets[e + 1] > a.offsets[e] && blockIdx.x * kExpRows < rows;
+    const bool live = a.s[m] != nullptr && a.offsets[e + 1] > a.offsets[e] && blockIdx.x * kExpRows<SLICES> < rows;
     if (live) {
         uint32_t v[4] = {0, 0, 0, 0};
         // magnitudes of two scales as 16-bit integers; infinities and NaN count as 0
@@ -656,14 +661,14 @@ w4_exponent_kernel(const ExpArgs a) {
         };
         if (row < rows) {
             const uint16_t* s = a.s[m] + (int64_t)e * a.ng[m] * rows + row;
-#pragma unroll 4
-            for (int g = slice; g < a.ng[m]; g += 16) take(v, __ldg(reinterpret_cast<const uint4*>(s + (int64_t)g * rows)));
+#pragma unroll 8
+            for (int g = slice; g < a.ng[m]; g += SLICES) take(v, __ldg(reinterpret_cast<const uint4*>(s + (int64_t)g * rows)));
         }
         sh[slice][l] = make_uint4(v[0], v[1], v[2], v[3]);
         __syncthreads();
-        if (threadIdx.x < 16 && row < rows) {
+        if (slice == 0 && row < rows) {
 #pragma unroll
-            for (int i = 1; i < 16; ++i) take(v, sh[i][l]);
+            for (int i = 1; i < SLICES; ++i) take(v, sh[i][l]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) big[i] = i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16;
             uint32_t out[2] = {0, 0};
@@ -682,9 +687,9 @@ w4_exponent_kernel(const ExpArgs a) {
     }
     pdl_wait();
     pdl_launch();
-    if (!live || m == 2 || threadIdx.x >= 32) return;
+    if (!live || m == 2 || threadIdx.x >= max(32, LANES)) return;   // whole warps with slice 0
     const uint32_t all = __reduce_max_sync(0xffffffffu, big[0]), b = __reduce_max_sync(0xffffffffu, bias);
-    if (threadIdx.x == 0) {   // a maximum: the order of arrival does not matter
+    if (threadIdx.x % 32 == 0) {   // a maximum: the order of arrival does not matter
         atomicMax(a.top + 2 * m * a.N + e, (int32_t)all);
         atomicMax(a.top + (2 * m + 1) * a.N + e, (int32_t)b);
     }
@@ -771,7 +776,10 @@ cudaError_t launch_w4_ffn_tc(const W4FfnArgs& a, cudaStream_t s) {
     ea.N = a.N;
     ea.top = a.top;
     const int most = a.d > a.d_ff ? a.d : a.d_ff;
-    err = launch_k(w4_exponent_kernel, dim3((unsigned)((most + kExpRows - 1) / kExpRows), (unsigned)a.N, 3u), dim3(256), 0, s, 1, ea);
+    auto exponents = [&](auto kern, int rows) {
+        return launch_k(kern, dim3((unsigned)((most + rows - 1) / rows), (unsigned)a.N, 3u), dim3(kExpThreads), 0, s, 1, ea);
+    };
+    err = a.group == 128 ? exponents(w4_exponent_kernel<4>, kExpRows<4>) : exponents(w4_exponent_kernel<16>, kExpRows<16>);
     if (err != cudaSuccess) return err;
     TcParams p{};
     p.offsets = a.offsets;
