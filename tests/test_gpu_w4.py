@@ -203,6 +203,18 @@ def test_expert_ffn_many_rows(act, group, d, dff, rows):
     assert torch.equal(y, run_ffn(dev, x, off, N, d, dff, group, act, off[-1] + 40)), "two runs differ"
 
 
+@pytest.mark.parametrize("act,group", [("swiglu", 128), ("relu", 64), ("swiglu", 32)])
+@pytest.mark.parametrize("rows", [[200, 216], [150, 170], [0, 440]])
+def test_many_rows_over_a_long_k(act, group, rows):
+    # K of more blocks than any ring of barriers is long, ending in the first half of a block (stage 1)
+    # and in the second (stage 2); 228 rows an expert on average are a tile of up to 256, 180 one of up to 192
+    N, d, dff, off = 2, 3216, 2640, [0, rows[0], sum(rows)]
+    W, dev = make_experts(N, d, dff, group, act, False, seed=group)
+    x = make_rows(off[-1], d)
+    y = run_ffn(dev, x, off, N, d, dff, group, act, off[-1] + 40)
+    check_ffn(W, x, y, off, group, act, rows=24)
+
+
 @pytest.mark.parametrize("act,group", [("relu", 128), ("swiglu", 32)])
 @pytest.mark.parametrize("N,d,dff,most", [
     (1, 128, 128, 16), (1, 128, 128, 17), (1, 16, 16, 40), (1, 48, 272, 193), (2, 272, 16, 33), (128, 64, 48, 5), (128, 16, 144, 40)])
