@@ -14,15 +14,18 @@
 // TMEM.  (bf16 integers as A, with every group's sum read back from TMEM and scaled
 // in registers, ran at 0.98 ms where this ran at 0.86: reading back was the
 // bottleneck.)  fp16's range is met by powers of two, which round nothing:
-//   weights: per row, so that its largest scale lies in [2^11, 2^12) -- exact for
-//     scales down to 2^-28 of it;
-//   x: per token, so that its largest value lies in [2^14, 2^15) -- exact for values
+//   weights: per row, so that its largest scale lies in [2^10, 2^12) -- exact for
+//     scales down to 2^-27 of it;
+//   x: per token, so that its largest value lies in [2^13, 2^15) -- exact for values
 //     down to 2^-29 of it (bf16 has eight bits);
 //   H: per token, from |u| <= (sum |x|) 8 max|s| and the biases, which no value
 //     passes.  The bound is about 2^8 (SwiGLU: 2^16) above typical values, whose fp16
-//     form has all its bits down to 2^-14 / 2^15 = 2^-29 of it; those give 2^-12, a
-//     sixteenth of the rounding to bf16 that the layer on bf16 weights applies here.
-// The epilogues undo the powers in fp32.
+//     form has all its bits down to 2^-14 / 2^14 = 2^-28 of it; those give 2^-11, an
+//     eighth of the rounding to bf16 that the layer on bf16 weights applies here.
+// The epilogues undo the powers in fp32.  All exponents are even: half of a row's and half
+// of a token's make a factor t = 2^((e + ex) / 2) that is always a normal number, and
+// (sum t) t leaves fp32 only where the result itself does (the sum is 0 or 2^-48 ... 2^53,
+// so sum t is subnormal or infinite only if sum t t is far below 2^-126 or above 2^128).
 //
 // Single-lane branches around TMA, MMA and commit use elect.sync in a warp-uniform
 // loop: with `lane == 0` each such instruction took 45 cycles to issue, not 9.
@@ -75,9 +78,6 @@ struct Shape {
     static constexpr int SMEM = WSTAGES * (kWBytes + kSBytes) + XSTAGES * XBYTES + 1024;
     static_assert(A == 2 && RING > XSTAGES && RING % XSTAGES == 0 && RING % (A * UPB) == 0, "the ring's indexes");
 };
-// Sums (up to 2^27 K) meet the row's power of two first: 2^-24 of it waits for the token's, so
-// that neither product leaves fp32's range for scales of 2^-91 .. 2^88 (K = 2^14) and x below 2^117.
-constexpr int kBalance = 24;
 constexpr int kNanExp = 0x7FFF;                   // exponent of a row that holds a NaN or infinity
 
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };
@@ -86,8 +86,8 @@ struct TcParams {
     const int32_t* offsets; int N; int64_t R_cap;
     int m_dim, k_dim;
     const __nv_bfloat16* bias_a; const __nv_bfloat16* bias_b;
-    const int8_t* ea; const int8_t* eb;   // [N, m_dim] row exponents: scales were taken times 2^-e
-    const int16_t* ex;                    // [R] exponents of the tokens' rows: x times 2^-ex
+    const int8_t* ea; const int8_t* eb;   // [N, m_dim] row exponents, -126 .. 116: scales were taken times 2^-e
+    const int16_t* ex;                    // [R] exponents of the tokens' rows, -126 .. 126: x times 2^-ex
     const int16_t* lx;                    // stage 1: [R] sum |x| < 2^lx
     const int32_t* top;                   // stage 1: [4][N] largest scale and bias of W1, W3 (as float bits)
     int16_t* eh;                          // stage 1: [R] exponents of H
@@ -137,12 +137,15 @@ __device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t w8, int p, 
     return *reinterpret_cast<const uint32_t*>(&q);
 }
 
-// 2^e for -126 <= e <= 127 (others clamped: 0 < 2^e < inf)
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((min(max(e, -126), 127) + 127) << 23); }
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// the next even exponent, up
+__device__ __forceinline__ int even(int e) { return (e + 1) & ~1; }
 // exponent of a finite positive float's leading bit (0 and subnormals: -127)
 __device__ __forceinline__ int exp_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
 
-// The exponent that brings a token's H to fp16 range: its bound's, less 15.
+// The exponent that brings a token's H to fp16 range: its bound's, less 15 (or 14).  A bound
+// past 2^141 takes 126 too: H itself, in fp32, is below 2^128.
 template <int EPI>
 __device__ __forceinline__ int h_exponent(const int32_t* top, int N, int e, int lx) {
     // |u| < 2^lx 8 2^(exp(max scale) + 1), plus the bias
@@ -150,7 +153,7 @@ __device__ __forceinline__ int h_exponent(const int32_t* top, int N, int e, int 
         const int u = lx + 3 + exp_of(top[2 * m * N + e]) + 1, b = exp_of(top[(2 * m + 1) * N + e]) + 1;
         return max(u, b) + 1;
     };
-    return min(max(side(0) + (EPI == W4_SWIGLU ? side(1) : 0) - 15, -126), 126);
+    return even(min(max(side(0) + (EPI == W4_SWIGLU ? side(1) : 0) - 15, -126), 126));
 }
 
 template <bool WIDE>
@@ -507,14 +510,14 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
             const bool in = feat < p.m_dim;
             const int n = t.n - c0;   // this group's tokens (may be none)
             const int64_t at = (int64_t)t.e * p.m_dim + feat;
-            const float up = pow2i((in ? exps[at] : 0) - kBalance);
+            const float up = pow2i((in ? exps[at] : 0) / 2);
             const float b = in && bias ? __bfloat162float(bias[at]) : 0.f;
-            // the powers of two of these tokens: x's, and H's
+            // the powers of two of these tokens: half of x's, and H's
             float* s_x = sh.scale[warp - 12][0];
             float* s_h = sh.scale[warp - 12][1];
             for (int c = lane; c < n && c < S::PART; c += 32) {
                 const int ex = p.ex[t.row0 + c0 + c];
-                s_x[c] = ex == kNanExp ? __int_as_float(0x7FC00000) : pow2i(ex + kBalance);
+                s_x[c] = ex == kNanExp ? __int_as_float(0x7FC00000) : pow2i(ex / 2);
                 if (EPI != W4_OUT) {
                     const int eh = h_exponent<EPI>(p.top, p.N, t.e, p.lx[t.row0 + c0 + c]);
                     s_h[c] = pow2i(-eh);
@@ -536,8 +539,9 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                     __half* dst = reinterpret_cast<__half*>(p.out) + row + (low ? 0 : p.m_dim);
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float v0 = fmaf(__uint_as_float(v[c]) * up, s_x[cb + c], b);
-                        const float v1 = fmaf(__uint_as_float(v[c + 1]) * up, s_x[cb + c + 1], b);
+                        const float t0 = up * s_x[cb + c], t1 = up * s_x[cb + c + 1];
+                        const float v0 = fmaf(__uint_as_float(v[c]) * t0, t0, b);
+                        const float v1 = fmaf(__uint_as_float(v[c + 1]) * t1, t1, b);
                         const float other = __shfl_xor_sync(0xffffffffu, low ? v1 : v0, 16);
                         const float gate = low ? v0 : other, val = low ? other : v1;
                         // e^-z -> inf for very negative z: the fast division gives the limit 0
@@ -548,7 +552,8 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
                 } else {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        float o = fmaf(__uint_as_float(v[c]) * up, s_x[cb + c], b);
+                        const float tc = up * s_x[cb + c];
+                        float o = fmaf(__uint_as_float(v[c]) * tc, tc, b);
                         if (EPI == W4_RELU) {
                             o = o < 0.f ? 0.f : o;   // NaN stays
                             if (in && cb + c < n)
@@ -595,7 +600,7 @@ w4_half_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
         }
         const uint32_t big = __reduce_max_sync(0xffffffffu, max(m >> 16, m & 0xFFFFu)) << 16;
         const bool finite = big < 0x7F800000u;
-        const int e = max(exp_of(big) - 14, -112);
+        const int e = even(max(exp_of(big) - 14, -112));
         const float down = finite ? pow2i(-e) : 0.f;
         if (lane == 0) ex[r] = (int16_t)(finite ? e : kNanExp);
         uint4* dst = reinterpret_cast<uint4*>(out + r * k_dim);
@@ -621,7 +626,7 @@ w4_half_rows_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restri
     }
 }
 
-// Every weight row's exponent: its largest finite scale times 2^-e lies in [2^11, 2^12);
+// Every weight row's exponent: its largest finite scale times 2^-e lies in [2^10, 2^12);
 // and of W1, W3 the largest scale and bias of the expert.  A thread takes eight rows and a
 // slice of the groups, eight loads in flight (a thread per row waited for one load after the
 // other: 37 us for the d_model 4096 layer's 22 MB of scales).  Four slices of groups of 128,
@@ -673,7 +678,7 @@ w4_exponent_kernel(const ExpArgs a) {
             for (int i = 0; i < 8; ++i) big[i] = i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16;
             uint32_t out[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) out[i / 4] |= (uint32_t)(max(exp_of(big[i]) - 11, -126) & 255) << (8 * (i & 3));
+            for (int i = 0; i < 8; ++i) out[i / 4] |= (uint32_t)(even(max(exp_of(big[i]) - 11, -126)) & 255) << (8 * (i & 3));
             *reinterpret_cast<uint2*>(a.e[m] + (int64_t)e * rows + row) = make_uint2(out[0], out[1]);
             if (m < 2 && a.b[m]) {
                 uint32_t b[4] = {0, 0, 0, 0};
