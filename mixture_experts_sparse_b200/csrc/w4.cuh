@@ -33,8 +33,8 @@ struct W4Mat {            // one weight matrix per expert: [N][rows][K]
 // are the B fragments of two k-steps: for t, j = 0..3, 0..1 the eight values k =
 // 32 j + 8 t .. + 7 at 16 t + 8 j, in the order 0 4 1 5 2 6 3 7 of the words'
 // nibbles.  Rows are padded to 256 values; units are fp32 [R][padded / 64] (a block of
-// 128 has its unit twice), divided by 16 (the weights' bytes are 16 q).  A block that holds a NaN or infinity has
-// unit NaN; magnitudes below 2^-100 count as 0.
+// 128 has its unit twice), divided by 16 (the weights' bytes are 16 q) and by 2^12 (range).  A block that holds a
+// NaN or infinity has unit NaN; a block whose largest magnitude is below 2^-100 counts as 0.
 constexpr int kW4ActBlock = 64;
 inline __host__ __device__ int64_t w4_padded(int64_t k) { return (k + 255) / 256 * 256; }
 

@@ -119,12 +119,16 @@ __device__ __forceinline__ void to_bytes(const float (&v)[8], float inv, uint2& 
     hi = make_uint2(h[0], h[1]);
     lo = make_uint2(l[0], l[1]);
 }
+// Units carry a further 2^-12, which the sums' readers take back: kMagicValue times a unit
+// and a block's sum (up to 128 x 8 values) stay finite for blocks up to bf16's and fp32's
+// largest.  From 2^-95 down units are subnormal, with 18 bits left at 2^-100.
+constexpr float kUnitDown = 1.f / 4096.f, kSumUp = 4096.f;
 // the unit (over 16) and its reciprocal for a block's largest magnitude, given as bits
 __device__ __forceinline__ void block_unit(uint32_t max_bits, float& unit16, float& inv) {
     const float m = __uint_as_float(max_bits);
     const bool finite = max_bits < 0x7F800000u, some = finite && m >= 7.8886e-31f;   // 2^-100
     inv = some ? 32512.f / m : 0.f;
-    unit16 = some ? m * (1.f / (16.f * 32512.f)) : (finite ? 0.f : __uint_as_float(0x7FC00000u));
+    unit16 = some ? m * (kUnitDown / (16.f * 32512.f)) : (finite ? 0.f : __uint_as_float(0x7FC00000u));
 }
 
 // 16 bytes global -> shared; ok = false fills zeros
@@ -456,14 +460,14 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const R
         const float ba = in && p.bias_a ? __bfloat162float(p.bias_a[bi]) : 0.f;
         const float bb = S::MATS == 2 && in && p.bias_b ? __bfloat162float(p.bias_b[bi]) : 0.f;
         for (int col = tid / S::FEATS; col < un.n; col += S::MATS) {
-            float o = s_out[col * kOutPitch + f] + ba;
+            float o = fmaf(s_out[col * kOutPitch + f], kSumUp, ba);
             if (EPI == W4_OUT) {
                 if (in) p.out[(int64_t)(un.row0 + col) * p.m_dim + feat] = __float2bfloat16_rn(o);
                 continue;
             }
             if (EPI == W4_RELU) o = o < 0.f ? 0.f : o;   // NaN stays
             if (EPI == W4_SWIGLU)
-                o = o / (1.f + fast_exp2(-o * kLog2e)) * (s_out[col * kOutPitch + S::FEATS + f] + bb);
+                o = o / (1.f + fast_exp2(-o * kLog2e)) * fmaf(s_out[col * kOutPitch + S::FEATS + f], kSumUp, bb);
             s_out[col * kOutPitch + f] = in ? o : 0.f;
         }
         if (EPI == W4_OUT) continue;

@@ -49,7 +49,7 @@ def case(act, rows, x_pow, group=64, bias=False, **powers):
     check(W, x, run_ffn(dev, x, off, N, d, dff, group, act, off[-1]), off, group, act)
 
 
-@pytest.mark.parametrize("rows", [MANY])
+@pytest.mark.parametrize("rows", [MANY, FEW])
 @pytest.mark.parametrize("group", [32, 128])
 @pytest.mark.parametrize("act,x_pow,powers", [
     # rows of x whose largest value is near 2^125, bf16's own largest being 2^128
@@ -59,12 +59,14 @@ def case(act, rows, x_pow, group=64, bias=False, **powers):
     # H near 2^121, its bound well past fp32
     ("swiglu", 62, dict(w2=-60)), ("relu", 20, dict(w1=100, w2=-60)),
     # both ends at once
-    ("relu", 120, dict(w1=-100, w2=-10)), ("relu", -80, dict(w1=100, w2=20))])
+    ("relu", 120, dict(w1=-100, w2=-10)), ("relu", -80, dict(w1=100, w2=20)),
+    # blocks of x whose units are subnormal in the few-row kernel
+    ("relu", -98, dict(w1=90))])
 def test_far_powers_of_two(rows, act, x_pow, powers, group):
     case(act, rows, x_pow, group, **powers)
 
 
-@pytest.mark.parametrize("rows", [MANY])
+@pytest.mark.parametrize("rows", [MANY, FEW])
 def test_rows_and_features_at_both_ends_of_one_tile(rows):
     # x from 2^-60 to 2^120 from row to row, weight rows from 2^-100 to 2^60 within the same tile
     N, d, dff, group = 2, 256, 320, 64
