@@ -309,6 +309,7 @@ balance_tile_kernel(const BalanceArgs a) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L, g = lane / L;
     const int N = a.N;
     for (int j = lane; j < 4 * C * L; j += 32) sh.cnt[warp][j] = 0;
+    __syncwarp();   // before any lane counts in them
     pdl_wait();
     if (!FUSED) pdl_launch();
     const int t0 = (int)blockIdx.x * a.tile, t1 = (int)min(a.T, (int64_t)t0 + a.tile);

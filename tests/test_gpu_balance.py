@@ -309,3 +309,13 @@ def test_router_gradient_of_the_balance_loss():
     for got, want in ((dh, total), (dw, total.T @ xv), (db, total.sum(0)), (dx, total @ L["w_r"].astype(np.float64))):
         # the router backward's own tolerance: 1e-5 of the largest magnitude
         assert np.abs(got.double().cpu().numpy() - want).max() <= 1e-5 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("N", [1, 2, 3, 4])
+@pytest.mark.parametrize("T", [1, 31, 257, 1025, 5000])
+def test_counts_of_few_experts_in_one_sequence(T, N):
+    # a row per lane and no sequence to look for: a warp's counters are cleared and counted in with
+    # no exchange between its lanes but the one that orders the two
+    h, idx, _, m = make(T, N, N, 1, "f32", seed=T + N)
+    for _ in range(5):
+        check(h, idx, None, m, "f32", run(h, idx, None, m, "f32"))
