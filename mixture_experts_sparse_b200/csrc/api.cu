@@ -521,7 +521,7 @@ static BalanceLayout balance_layout(const moe_balance_config& c) {
     };
     const size_t slots = (size_t)balance_slots(c.T, c.n_experts, c.n_seqs), N = (size_t)c.n_experts, S = (size_t)c.n_seqs;
     L.hdr = take(sizeof(WsHeader));
-    L.slot_p = take(4 * slots * N);
+    L.slot_p = take(8 * slots * N);
     L.slot_c = take(4 * slots * N);
     L.slot_z = take(8 * slots);
     L.slot_n = take(4 * slots);
@@ -570,7 +570,7 @@ int32_t moe_balance_loss(const moe_balance_config* cfg, const void* logits, cons
     a.counts = counts;
     a.P = P;
     a.tokens = tokens;
-    a.slot_p = at<float>(ws, L.slot_p);
+    a.slot_p = at<double>(ws, L.slot_p);
     a.slot_c = at<int32_t>(ws, L.slot_c);
     a.slot_z = at<double>(ws, L.slot_z);
     a.slot_n = at<int32_t>(ws, L.slot_n);

@@ -27,9 +27,11 @@
 // cut it.  The share of (tile b, sequence s) goes to slot b + s of the
 // workspace: both indexes only grow along the tokens, so no two shares meet,
 // and a reducer finds its sequence's shares without a list.  Sums of p run in
-// fp32 over a lane's own tokens, then in fixed order (warp tree, warps, tiles in
+// fp32 over a lane's own tokens, then in fixed order (warp, warps, tiles in
 // fp64); counts are integers.  Nothing depends on the order of arrival.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -185,7 +187,7 @@ __device__ __forceinline__ void sum_unit(const BalanceArgs& a, int unit, SumShar
     if (e < N) {
 #pragma unroll 8
         for (int b = b0 + warp; b < b1; b += Ways) {
-            p += (double)__ldcg(a.slot_p + (int64_t)(b + s) * N + e);
+            p += __ldcg(a.slot_p + (int64_t)(b + s) * N + e);
             c += __ldcg(a.slot_c + (int64_t)(b + s) * N + e);
         }
     }
@@ -292,20 +294,60 @@ balance_sum_kernel(const BalanceArgs a) {
 
 // ---- one pass over the tokens -------------------------------------------------
 
-template <int W> struct TileShared {   // W experts, padded
-    float p[kBalWarps][W];
+// W experts, padded.  A warp's sum of p: of its row groups in fp64, or (one group, L = 32) its lane's own.
+template <int W, int L> struct TileShared {
+    std::conditional_t<L == 32, float, double> p[kBalWarps][W];
     int cnt[kBalWarps][W];
     double z[kBalWarps];
     int n[kBalWarps];
 };
 
-// FUSED: the tile that finishes last also sums, without a second launch
+// Sums of a lane's N columns over the row groups that lane bits O ... L tell apart.  A step halves the
+// columns that a lane adds up (its partner takes the others); with one left the groups only add.
+template <int L, int O, int N, int M, typename P>
+__device__ __forceinline__ void fold(P (&p)[M], int lane, int& first, bool& writes) {
+    if constexpr (O >= L) {
+        const bool upper = lane & O;
+        if constexpr (N > 1) {
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const P give = upper ? p[j] : p[j + N / 2];
+                p[j] = (upper ? p[j + N / 2] : p[j]) + __shfl_xor_sync(0xffffffffu, give, O);
+            }
+            first += upper ? N / 2 : 0;
+        } else {
+            p[0] += __shfl_xor_sync(0xffffffffu, p[0], O);
+            writes = writes && !upper;
+        }
+        fold<L, O / 2, (N > 1 ? N / 2 : 1)>(p, lane, first, writes);
+    }
+}
+
+// acc over a warp's 32 / L row groups, in fp64, into out by column: 16 columns over 8 groups take 14
+// exchanges and not 48 (65536 rows of 64: 15.6 us for 16.7)
+template <int L, int C, bool VEC, typename P>
+__device__ __forceinline__ void sum_groups(const float (&acc)[4 * C], int lane, int l, P* out) {
+    constexpr int G = 32 / L, N = 4 * C > G ? 4 * C / G : 1;   // columns a lane ends with
+    P p[4 * C];
+#pragma unroll
+    for (int j = 0; j < 4 * C; ++j) p[j] = acc[j];
+    int first = 0;
+    bool writes = true;
+    fold<L, 16, 4 * C>(p, lane, first, writes);
+    if (writes) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) out[col_of<L, C, VEC>(l, (first + j) / 4, (first + j) % 4)] = p[j];
+    }
+}
+
+// FUSED: the tile that finishes last also sums, without a second launch (few tiles: one CTA
+// per SM, and registers enough not to spill)
 template <typename T, int L, int C, bool VEC, bool FUSED>
-__global__ void __launch_bounds__(kBalThreads, kBalPerSm)
+__global__ void __launch_bounds__(kBalThreads, FUSED ? 1 : kBalPerSm)
 balance_tile_kernel(const BalanceArgs a) {
     using B = Batch<T, L, C, VEC>;
     constexpr int U = B::U;
-    __shared__ TileShared<4 * C * L> sh;
+    __shared__ TileShared<4 * C * L, L> sh;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, l = lane % L, g = lane / L;
     const int N = a.N;
     for (int j = lane; j < 4 * C * L; j += 32) sh.cnt[warp][j] = 0;
@@ -346,17 +388,10 @@ balance_tile_kernel(const BalanceArgs a) {
         if (max(t0, q0) >= min(t1, q1)) return;   // no row of it in the tile
 #pragma unroll
         for (int o = L; o < 32; o <<= 1) {
-#pragma unroll
-            for (int j = 0; j < 4 * C; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
             z += __shfl_xor_sync(0xffffffffu, z, o);
             n += __shfl_xor_sync(0xffffffffu, n, o);
         }
-        if (g == 0) {
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) sh.p[warp][col_of<L, C, VEC>(l, c, i)] = acc[4 * c + i];
-        }
+        sum_groups<L, C, VEC>(acc, lane, l, sh.p[warp]);
         if (lane == 0) {
             sh.z[warp] = z;
             sh.n[warp] = n;
@@ -372,7 +407,7 @@ balance_tile_kernel(const BalanceArgs a) {
                 c += sh.cnt[w][e];
                 sh.cnt[w][e] = 0;
             }
-            a.slot_p[slot * N + e] = (float)p;
+            a.slot_p[slot * N + e] = p;
             a.slot_c[slot * N + e] = c;
         }
         if (warp == kBalWarps - 1) {

@@ -257,7 +257,7 @@ struct BalanceArgs {
     int64_t T; int N; int k; int S; int tile;
     float alpha; float z_coef;
     float* loss; int32_t* counts; float* P; int32_t* tokens;
-    float* slot_p; int32_t* slot_c; double* slot_z; int32_t* slot_n;   // [balance_slots(T, S)](, N)
+    double* slot_p; int32_t* slot_c; double* slot_z; int32_t* slot_n;   // [balance_slots(T, N, S)](, N)
     double* seq_term; double* seq_z;          // [S, ceil(N / 32)], [S]
     int32_t* ticket;
     const float* dloss; void* dh; int64_t dld; bool accumulate;

@@ -319,3 +319,19 @@ def test_counts_of_few_experts_in_one_sequence(T, N):
     h, idx, _, m = make(T, N, N, 1, "f32", seed=T + N)
     for _ in range(5):
         check(h, idx, None, m, "f32", run(h, idx, None, m, "f32"))
+
+
+@pytest.mark.parametrize("T,N,dtype", [(2300, 512, "f32"), (1111, 256, "f32"), (1500, 64, "bf16"), (700, 33, "f32")])
+def test_sums_of_p_past_a_lane_run_in_64_bits(T, N, dtype):
+    # every tile is one row per lane, so no two values of p meet in fp32: P and the loss are one
+    # rounding (2^-24) of the fp64 sums of the kernel's own p, which single-row sequences give.
+    # Each further rounding of a tile's share to fp32 would be as large.
+    h, idx, _, _ = make(T, N, 1, 1, dtype, seed=T, mask=False)
+    alone = run(h, idx, np.arange(T + 1, dtype=np.int32), None, dtype)
+    p = alone["P"].double().numpy()
+    o = run(h, idx, None, None, dtype, alpha=0.25, zc=0.0)
+    mean = p.mean(axis=0)
+    one = 2.0 ** -24 * (1 + 2.0 ** -20)   # fp64's own rounding: T 2^-53
+    assert (np.abs(o["P"].double().numpy()[0] - mean) <= one * mean).all()
+    aux = 0.25 * N * (o["counts"].double().numpy()[0] / T * mean).sum()
+    assert abs(o["loss"][0].item() - aux) <= one * aux
