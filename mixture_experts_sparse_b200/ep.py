@@ -104,7 +104,7 @@ class EpRank:
         self.ws = nat.new_workspace(self.cfg, device)
         self.w_r, self.b_r = w_r, b_r
         self.w = local_weights                 # this GPU's experts: w1 [E, d_ff, d] ...
-        act_t = torch.bfloat16 if dtype == "bf16" else torch.float32
+        act_t = torch.bfloat16 if self.cfg.dtype == nat.MOE_BF16 else torch.float32
         i32, f32, f64 = torch.int32, torch.float32, torch.float64
         N, k, d = n_experts, top_k, d_model
         R = max(1, min(k * T, N * C))

@@ -40,7 +40,7 @@ class MoeLayer:
         self.device = device
         self.w = {k: to_device(weights.get(k), device) for k in WEIGHT_KEYS}
         self.ws = nat.new_workspace(self.cfg, device)
-        self.act_dtype = torch.bfloat16 if dtype == "bf16" else torch.float32
+        self.act_dtype = torch.bfloat16 if self.cfg.dtype == nat.MOE_BF16 else torch.float32
         i32, f32, f64 = torch.int32, torch.float32, torch.float64
         k, N = top_k, n_experts
         self.out = torch.empty(T, d_model, dtype=self.act_dtype, device=device)

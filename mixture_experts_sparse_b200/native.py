@@ -108,12 +108,25 @@ def lib():
 MOE_ORDER_TOKEN, MOE_ORDER_PRIORITY, MOE_ORDER_NTLB = 0, 1, 2
 
 
+def _dt(dtype):
+    """moe_dtype of "f32" / "bf16", their moe_dtype or torch dtype.  The kernels get bare
+    pointers: a type read as another would send them past a buffer's end."""
+    if isinstance(dtype, int):
+        if dtype in (MOE_F32, MOE_BF16):
+            return int(dtype)
+    elif str(dtype) in ("f32", "torch.float32"):
+        return MOE_F32
+    elif str(dtype) in ("bf16", "torch.bfloat16"):
+        return MOE_BF16
+    raise ValueError(f"dtype {dtype!r}: expected 'f32' or 'bf16'")
+
+
 def config(T, d_model, d_ff, n_experts, top_k, capacity, dtype="bf16", act="relu", alpha=1e-2, priority=False):
     """moe_config.  priority: False/MOE_ORDER_TOKEN, True/MOE_ORDER_PRIORITY
     (batch priority) or MOE_ORDER_NTLB (No-Token-Left-Behind re-routing)."""
     order = MOE_ORDER_PRIORITY if priority is True else (MOE_ORDER_TOKEN if priority is False else int(priority))
     return MoeConfig(int(T), int(d_model), int(d_ff), int(n_experts), int(top_k), int(capacity),
-                     MOE_BF16 if dtype in ("bf16", MOE_BF16) else MOE_F32,
+                     _dt(dtype),
                      MOE_SWIGLU if act in ("swiglu", MOE_SWIGLU) else MOE_RELU, float(alpha), order)
 
 
@@ -290,10 +303,6 @@ def moe_expert_ffn(cfg, xe, offsets, w1, b1, w3, b3, w2, b2, ye, ws, stream=None
 
 
 # ---- 4-bit expert weights
-
-def _dt(dtype):
-    return MOE_BF16 if dtype in ("bf16", MOE_BF16) else MOE_F32
-
 
 def moe_w4_row_bytes(k):
     return int(lib().moe_w4_row_bytes(int(k)))

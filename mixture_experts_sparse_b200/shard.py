@@ -39,7 +39,7 @@ class Shard:
         self.ws = nat.new_workspace(self.cfg, device)
         T, k, N, d = T_shard, top_k, n_experts, d_model
         R = max(1, min(k * T, N * C_group))
-        act_t = torch.bfloat16 if dtype == "bf16" else torch.float32
+        act_t = torch.bfloat16 if self.cfg.dtype == nat.MOE_BF16 else torch.float32
         i32, f32, f64 = torch.int32, torch.float32, torch.float64
         self.T, self.N, self.k, self.alpha = T, N, k, alpha
         self.idx = torch.empty(T, k, dtype=i32, device=device)

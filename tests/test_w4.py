@@ -107,3 +107,18 @@ def test_bad_forward_calls_are_refused():
         assert fwd(**{name: None}) == nat.MOE_ERR_INVALID_ARG, name
     assert fwd(group=0) == nat.MOE_ERR_UNSUPPORTED
     assert fwd(nbytes=nat.moe_workspace_bytes(cfg)) == nat.MOE_ERR_WORKSPACE   # the bf16 layer's is too small
+
+
+def test_names_of_types():
+    torch = pytest.importorskip("torch")
+    for name in ("f32", nat.MOE_F32, torch.float32):
+        assert nat._dt(name) == nat.config(4, 16, 16, 2, 1, 4, name).dtype == nat.balance_config(4, 2, 1, 1, name).dtype == nat.MOE_F32
+    for name in ("bf16", nat.MOE_BF16, torch.bfloat16):
+        assert nat._dt(name) == nat.config(4, 16, 16, 2, 1, 4, name).dtype == nat.balance_config(4, 2, 1, 1, name).dtype == nat.MOE_BF16
+    # taken for fp32, each of these would have the kernels read and write past a buffer's end
+    for name in ("bfloat16", "f16", "fp16", torch.float16, torch.int32, np.float32, 2, -1, None):
+        for call in (lambda: nat.config(4, 16, 16, 2, 1, 4, name), lambda: nat.balance_config(4, 2, 1, 1, name),
+                     lambda: nat.moe_quantize_w4(1, 4, 64, 32, name, None, None, None, 0),
+                     lambda: nat.moe_dequantize_w4(1, 4, 64, 32, name, None, None, None, 0)):
+            with pytest.raises(ValueError):
+                call()
