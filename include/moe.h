@@ -412,16 +412,23 @@ size_t moe_w4_workspace_bytes(const moe_config* cfg);
  * (q1, s1), (q3, s3; SwiGLU), (q2, s2), all with the same group; the biases are
  * bf16 (nullable).  bf16 rows in and out (MOE_F32: MOE_ERR_UNSUPPORTED).  Weights
  * enter as integers times their scale, unrounded, with fp32 accumulation; rows of
- * ye past offsets[N] are left as they were.  With up to 16 rows of capacity per
- * expert (min(k T, N C) <= 16 N) xe and H are rounded to 16-bit integers in blocks
- * of 64 or 128 values, to 2^-16 of a block's largest (a block below 2^-100 counts as
- * 0).  With more, xe is exact (down to 2^-29 of its row's largest) and H is fp16
- * times a power of two per row, taken from the bound sum |x| 8 max |s| (s: all scales
- * of the expert) and the biases: values below 2^-28 of that bound (for SwiGLU, of both
- * matrices' bounds' product) lose bits, and scales below 2^-27 of their weight row's
- * largest do.  No power of two taken on the way leaves fp32 where x W1, x W3, H and y
- * do not.  Infinities and NaN in a row of xe make that row of ye NaN or infinite, and
- * no other row. */
+ * ye past offsets[N] are left as they were. What xe
+ * and H keep depends on the capacity R = min(k T, N C):
+ *   R <= 16 N: both are rounded to 16-bit integers in blocks of 64 or 128 values, to
+ *     2^-16 of a block's largest (a block below 2^-100 counts as 0).  Values below
+ *     1/128 of it keep fewer bits than bf16 has: where one value per block is 300
+ *     (1000) times the others and meets zero weights, the products of the others are
+ *     off by 0.27% (0.9%) RMS, beside 0.17% from y's own rounding to bf16.  A caller
+ *     who cannot have that gives a configuration with more capacity.
+ *   R > 16 N: xe is exact (down to 2^-29 of its row's largest).  H is fp16 times a
+ *     power of two per row, taken from the bound sum |x| 8 max |s| (s: all scales of
+ *     the expert) and the biases: values below 2^-28 of that bound (for SwiGLU, of
+ *     both matrices' bounds' product) lose bits, so scales far above an expert's
+ *     others take some from every feature; scales below 2^-27 of their weight row's
+ *     largest lose bits too.
+ * No power of two taken on the way leaves fp32 where x W1, x W3, H and y do not.
+ * Infinities and NaN in a row of xe make that row of ye NaN or infinite, and no
+ * other row. */
 int32_t moe_expert_ffn_w4(const moe_config* cfg, int32_t group, const void* xe, const int32_t* offsets,
                           const uint8_t* q1, const void* s1, const void* b1, const uint8_t* q3, const void* s3,
                           const void* b3, const uint8_t* q2, const void* s2, const void* b2, void* ye,
