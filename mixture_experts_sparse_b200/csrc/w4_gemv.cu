@@ -46,6 +46,8 @@ constexpr int kStageK = kStageBlocks * kW4Block;
 constexpr int kWBytes = kRows * kStageBlocks * kW4BlockBytes;   // 16 KB
 constexpr int kOutPitch = kRows + 8;             // conflict-free accumulator writes
 constexpr int kMaxStages = 8;
+// 128 registers a thread: up to 12 bytes are spilled in stage 1 of ReLU with groups of 64 and in
+// stage 2 of SwiGLU with groups of 64 and 128.
 constexpr int kCtasPerSm = 3;
 constexpr int kSmem = 72 * 1024;                 // of a CTA
 constexpr int kBoxRows = 64, kBoxBytes = kBoxRows * 128;       // one TMA box of weights
@@ -83,8 +85,8 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // The first product of a block: c = kMagic + a b.  As bits of a float that is
-// 1.5 2^23 + the sum, exact while the sum stays below 2^22 (64 products of at most
-// 128 x 128 are 2^20): the conversion to fp32 is one subtraction.
+// 1.5 2^23 + the sum, exact while the sum stays below 2^22 (up to 128 products of at
+// most 128 x 128 are 2^21): the conversion to fp32 is one subtraction.
 constexpr int kMagic = 0x4B400000;
 __device__ __forceinline__ void mma_s8_first(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                              uint32_t b1) {
@@ -441,8 +443,8 @@ __device__ __forceinline__ void consume(const GemvParams& p, Shared& sh, const R
             if (!sh.last) continue;
             for (int col = 0; col < un.n; ++col) {   // in K order, eight loads at a time
                 const float* src = p.part + col * kRows + tid;
-                float v = __ldcg(src + ((int64_t)c0 * 2 + (pl.begin(c0) > u0 ? 0 : 1)) * kPartFloats);
-                for (int c = c0 + 1; c <= c1; c += 8) {   // the later parts start inside the tile: slot 0
+                float v = __ldcg(src + ((int64_t)c0 * 2 + 1) * kPartFloats);   // c0's part starts the tile: slot 1
+                for (int c = c0 + 1; c <= c1; c += 8) {                        // the later ones start inside it: slot 0
                     float q[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) q[i] = c + i <= c1 ? __ldcg(src + (int64_t)(c + i) * 2 * kPartFloats) : 0.f;

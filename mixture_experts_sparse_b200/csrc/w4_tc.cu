@@ -3,9 +3,9 @@
 //   stage 1: H = relu(x W1^T + b1), or silu(x W1^T + b1) * (x W3^T + b3)
 //   stage 2: y = H W2^T + b2              W[o][k] = q[o][k] s[o][k / G]
 //
-// The weights are the A operand: a tile is 128 weight rows by up to 192 tokens, so
-// each word is decoded once for 192 tokens, and a thread that decodes owns one
-// row.  Decoded words go straight into TMEM (tcgen05.st), from where tcgen05.mma
+// The weights are the A operand: a tile is 128 weight rows by up to 192 tokens, or by
+// up to 256 (see Shape), so each word is decoded once for all of them, and a thread that
+// decodes owns one row.  Decoded words go straight into TMEM (tcgen05.st), from where tcgen05.mma
 // reads A: through shared memory the operand would be written and read again
 // beside the tokens' tiles, more than the 128 bytes a cycle shared memory has.
 //
@@ -124,8 +124,9 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Weights 2 p and 2 p + 1 of a word's eight, times the scale s2 (an fp16 pair):
-// 0x6400 is 1024 in fp16, whose last place is 1, so nibbles in the low bits add to it
+// Weights 2 p and 2 p + 1 of a word's eight, times the scale s2 (an fp16 pair), by the known
+// way of joining integers to a float's low mantissa bits (for 4-bit experts: Kim, Henry, Fahim
+// and Hassan Awadalla, "Who Says Elephants Can't Run", 2022): 0x6400 is 1024 in fp16, whose last place is 1, so nibbles in the low bits add to it
 // exactly, and in bits 4-7 as sixteenfold; w8 = w >> 8 holds the odd pairs.
 __device__ __forceinline__ uint32_t decode_pair(uint32_t w, uint32_t w8, int p, __half2 s2) {
     uint32_t u;   // one operation: written as two immediates it would be two
@@ -495,7 +496,7 @@ w4_tc_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ 
         }
     } else {
         // ---------------- write out: lane = weight row ----------------
-        // two groups of four warps, 96 of the tile's tokens each
+        // two groups of four warps, half of the tile's tokens each (96, or 128 of a wide one)
         const int quad = warp & 3, c0 = (warp - 12) / 4 * S::PART;
         const int f = MATS == 2 ? quad * 16 + (lane & 15) : quad * 32 + lane;   // feature of the tile
         const bool low = lane < 16;
