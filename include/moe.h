@@ -223,7 +223,9 @@ int32_t moe_router_backward_dh(const moe_config* cfg, const void* x, const float
  * A sum without terms is 0.  A logit of -inf is an expert that cannot be
  * chosen (p = 0); a row without a finite logit counts in n_s and counts and
  * adds 0 to P and both losses; NaN or +inf make their token's terms NaN.  Choices
- * outside [0, N) are not counted.  Offsets outside [0, T] are clamped. */
+ * outside [0, N) are not counted.  Counts are 32 bits: an expert's choices within a
+ * sequence stay below 2^31, as they do where a token's choices differ.  Offsets
+ * outside [0, T] are clamped. */
 typedef struct {
     int32_t T;            /* rows of the batch */
     int32_t n_experts;    /* N */

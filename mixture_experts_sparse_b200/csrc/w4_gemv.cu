@@ -55,8 +55,9 @@ constexpr int kMinSteps = 2;                     // stages per CTA at least, whe
 constexpr int kIdleSteps = 8;                    // see the plan
 constexpr int kPartFloats = 8 * kRows;          // one fp32 part of a tile
 
-// Rows per expert, on average, up to which this kernel is used: at 12 it takes 258 us where w4_tc.cu
-// takes 370 (d_model 4096, d_ff 14336, 8 SwiGLU experts), at 16 281 and 371, at 24 465 and 378.
+// Rows per expert of the capacity, on average, up to which this kernel is used: at 12 it takes 261 us,
+// at 16 279 and at 24 465, where w4_tc.cu takes 356 (d_model 4096, d_ff 14336, 8 SwiGLU experts with
+// as many rows each).
 constexpr int kFewRows = 16;
 
 enum { W4_RELU = 0, W4_SWIGLU = 1, W4_OUT = 2 };

@@ -12,7 +12,7 @@
 // Operands are fp16, because q s (three bits times a bf16 scale's eight) is exact in
 // its eleven and not in bf16's eight; everything then accumulates over all of K in
 // TMEM.  (bf16 integers as A, with every group's sum read back from TMEM and scaled
-// in registers, ran at 0.98 ms where this ran at 0.86: reading back was the
+// in registers, took 0.98 ms where this, at the time, took 0.86: reading back was the
 // bottleneck.)  fp16's range is met by powers of two, which round nothing:
 //   weights: per row, so that its largest scale lies in [2^10, 2^12) -- exact for
 //     scales down to 2^-27 of it;
@@ -29,9 +29,9 @@
 //
 // Single-lane branches around TMA, MMA and commit use elect.sync in a warp-uniform
 // loop: with `lane == 0` each such instruction took 45 cycles to issue, not 9.
-// 1024 tokens of the d_model 4096 layer, 256 rows an expert on average: 0.70 ms, 1.0
-// PFLOP/s; the same rows spread evenly 0.60 ms.  With few tokens a tile (32 rows an
-// expert: 0.37 ms) a block's hand-overs between the roles bound it, not its MMAs.
+// 256 rows for each of 8 experts, d_model 4096, d_ff 14336: 0.63 ms, 1.14 PFLOP/s; 1024
+// tokens routed unevenly, inputs changing: 0.83 ms, 0.87 PFLOP/s.  With few tokens a tile (32
+// rows an expert: 0.36 ms) a block's hand-overs between the roles bound it, not its MMAs.
 //
 // Roles (five warpgroups): warps 0 and 3 TMA of the tokens' rows, 1 MMA issue, 2 TMA
 // of the packed rows and scales (they come from HBM and are asked for further ahead);
